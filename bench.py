@@ -140,13 +140,16 @@ def load_peaks():
 
 
 def source_hash() -> str:
-    """Hash of the kernel sources: the files that define kernels and the headers
-    they include (the host-only ABI code does not change what a kernel reads or
-    writes, so DRAM counters taken before an edit there still hold)."""
+    """Hash of the mixer's kernel sources: the files that define its kernels and the
+    headers they include (the host-only ABI code does not change what a kernel reads
+    or writes, so DRAM counters taken before an edit there still hold; the gated scan
+    and the state cache are not part of the mixer's path)."""
     import hashlib
     h = hashlib.sha256()
     d = os.path.join(ROOT, "mamba_ssd_scan_mixer_b200", "csrc")
     for f in sorted(os.listdir(d)):
+        if f.startswith(("gated_scan", "state_cache")):
+            continue
         with open(os.path.join(d, f), "rb") as fh:
             text = fh.read()
         if f.endswith(".cuh") or b"__global__" in text:

@@ -252,8 +252,10 @@ MAMBA2_API int mamba2_ssd_step(const mamba2_dims *dims, const mamba2_params *par
  * call undefined.  This call synchronises the current device, stores the
  * flags raised since the previous call in *flags (0 = none; bit 0 = a wait
  * ran out; bit 1 = the bounds-checked build skipped an access; bit 2 = a
- * packed-sequence prefill got invalid cu_seqlens) and clears them.  Returns MAMBA2_OK, MAMBA2_ERR_INVALID_ARG (flags
- * NULL) or MAMBA2_ERR_CUDA. */
+ * packed-sequence prefill, or a packed call of the gated scan, got invalid
+ * cu_seqlens; bit 3 = a state cache call got a slot beyond the cache) and clears
+ * them.  Returns MAMBA2_OK, MAMBA2_ERR_INVALID_ARG (flags NULL) or
+ * MAMBA2_ERR_CUDA. */
 MAMBA2_API int mamba2_device_errors(unsigned int *flags);
 
 /* Test aid (no counterpart on the pages): makes the time limit of a kernel's
@@ -355,6 +357,141 @@ MAMBA2_API int mamba2_conv_ssd_prefill_backward(
     float *d_conv_b, float *d_dt_bias, float *d_A, float *d_D, float *d_norm_w,
     void *d_conv_state_in, float *d_ssm_state_in, void *workspace, size_t workspace_bytes,
     void *stream);
+
+/* ------------------------------------------------------------------------
+ * Gated linear recurrence (no counterpart on the pages): the per-channel
+ * companion of the SSD scan, for layers whose state is one value a channel and
+ * whose decay is computed from the token.  With s = softplus(lam),
+ * R = sigmoid(r), G = sigmoid(g) and c = decay_scale,
+ *     a_t = exp(-c s R_t)
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) G_t x_t
+ *     y_t = h_t, or h_t silu(z_t) where a gate z is given.
+ * x, r, g and z are the layer's projections, biases included.  The state is
+ * fp32 and owned by the caller, as the SSM state is. */
+
+/* Tokens of a checkpoint (see mamba2_gated_scan_prefill). */
+#define MAMBA2_GATED_SCAN_CHUNK 128
+
+typedef struct {
+  int64_t batch;     /* b >= 0: sequences */
+  int64_t seqlen;    /* L >= 0: tokens of each, or of all of them in packed rows; step: ignored */
+  int32_t width;     /* D: channels, a multiple of 8, at most 2^20 */
+  int32_t io_dtype;  /* mamba2_dtype of x, r, g, z, y and their gradients */
+  float decay_scale; /* c > 0, e.g. 8 */
+} mamba2_gated_scan_dims;
+
+/* Workspace bytes of the prefill and of the backward pass (0 if the dims are
+ * invalid); packed != 0 for calls with cu_seqlens. */
+MAMBA2_API size_t mamba2_gated_scan_workspace_size(const mamba2_gated_scan_dims *dims, int packed);
+MAMBA2_API size_t mamba2_gated_scan_backward_workspace_size(const mamba2_gated_scan_dims *dims,
+                                                            int packed);
+
+/* fp32 values of the checkpoints of a prefill: rows * ceil(L / 128) * D, rows =
+ * batch, or 1 for packed rows (0 if the dims are invalid). */
+MAMBA2_API size_t mamba2_gated_scan_checkpoint_count(const mamba2_gated_scan_dims *dims,
+                                                     int packed);
+
+/* Prefill over L new tokens of each sequence.
+ *
+ *  lam     [D] fp32.
+ *  x, r, g, z  [b, L, D] io_dtype; token t of row bi starts at (bi * L + t) *
+ *          row_stride elements (stride >= D, a multiple of 8; pointer 16-byte
+ *          aligned), so they may be columns of one projection.  z may be NULL:
+ *          no output gate.
+ *  cu_seqlens  NULL, or device int32 [batch + 1]: the sequences are packed along
+ *          the token axis (x, ... are [L, D], y too) and sequence s owns tokens
+ *          cu_seqlens[s] .. cu_seqlens[s + 1] - 1: 0, then the running counts,
+ *          last = L; empty sequences are allowed.  Offsets that break this are
+ *          found on the device: the call then writes nothing and
+ *          mamba2_device_errors reports bit 2.
+ *  y       [b, L, D] io_dtype, contiguous, 16-byte aligned.  Output.
+ *  h_state [b, D] fp32, contiguous, 16-byte aligned, or NULL: when states_in != 0
+ *          the state entering the first token (else it is zero); on return the
+ *          state after the last.  A sequence without tokens keeps its state (or
+ *          gets zero).
+ *  checkpoints  NULL, or fp32 [rows, ceil(L / 128), D], 16-byte aligned: receives
+ *          the state entering tokens 0, 128, 256, ... of each row, for the
+ *          backward pass.  (In packed rows it is the state left by the token
+ *          before, whatever its sequence; token 0's is zero.)
+ *  workspace  >= mamba2_gated_scan_workspace_size bytes, 256-byte aligned;
+ *          contents on entry are ignored.  stream: cudaStream_t as void*.
+ * Results do not depend on timing: every sum has a fixed order. */
+MAMBA2_API int mamba2_gated_scan_prefill(
+    const mamba2_gated_scan_dims *dims, const float *lam, const void *x, int64_t x_row_stride,
+    const void *r, int64_t r_row_stride, const void *g, int64_t g_row_stride, const void *z,
+    int64_t z_row_stride, const int32_t *cu_seqlens, void *y, float *h_state, int32_t states_in,
+    float *checkpoints, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Decode: one token of each sequence.  x, r, g, z: [b, D] as above; y [b, D]
+ * contiguous; h_state [b, D] fp32, updated in place.  Uses no workspace. */
+MAMBA2_API int mamba2_gated_scan_step(const mamba2_gated_scan_dims *dims, const float *lam,
+                                      const void *x, int64_t x_row_stride, const void *r,
+                                      int64_t r_row_stride, const void *g, int64_t g_row_stride,
+                                      const void *z, int64_t z_row_stride, void *y, float *h_state,
+                                      void *stream);
+
+/* Backward pass of the prefill: the gradients of
+ *     sum(y * dy) + sum(h_state_out * d_h_state_out)
+ * with respect to every input, lam and the initial state.
+ *
+ *  dims ... cu_seqlens  as for the prefill.
+ *  h_state_in  [b, D] fp32 or NULL (zero): the state that the prefill began with.
+ *  dy      [b, L, D] io_dtype, contiguous, 16-byte aligned.
+ *  d_h_state_out  [b, D] fp32 or NULL (zero).
+ *  checkpoints  those of the prefill, or NULL: the scan is then run again here.
+ * Outputs, overwritten:
+ *  d_x, d_r, d_g, d_z  [b, L, D] io_dtype, contiguous, 16-byte aligned (d_z only
+ *          with z, else NULL); d_lam [D] fp32; d_h_state_in [b, D] fp32 or NULL.
+ * All states and their gradients are 16-byte aligned.  With invalid cu_seqlens
+ * nothing is written (bit 2 as above).  Results do not depend on timing. */
+MAMBA2_API int mamba2_gated_scan_backward(
+    const mamba2_gated_scan_dims *dims, const float *lam, const void *x, int64_t x_row_stride,
+    const void *r, int64_t r_row_stride, const void *g, int64_t g_row_stride, const void *z,
+    int64_t z_row_stride, const int32_t *cu_seqlens, const float *h_state_in, const void *dy,
+    const float *d_h_state_out, const float *checkpoints, void *d_x, void *d_r, void *d_g,
+    void *d_z, float *d_lam, float *d_h_state_in, void *workspace, size_t workspace_bytes,
+    void *stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit state cache (no counterpart on the pages): recurrent states (the SSM
+ * state, the conv state, the gated scan's state) put aside in slots of a cache,
+ * to be continued from later or by several sequences, in a quarter of fp32's
+ * bytes.  Each block of consecutive values of a state shares a scale 2^e, the
+ * least power of two with max |v| <= qmax 2^e (qmax = 127 for int8, 448 for
+ * e4m3), kept as the byte e + 127 (at least 0); a value is its code, v 2^-e
+ * rounded to nearest even, times 2^e.  Reading a slot back and writing it again
+ * gives the same values.  A block with an infinity or NaN gets the byte 255 and
+ * reads back as NaN. */
+typedef enum {
+  MAMBA2_CODES_INT8 = 0,
+  MAMBA2_CODES_E4M3 = 1
+} mamba2_code_format;
+
+typedef struct {
+  int64_t batch;       /* b >= 0, at most 65535: working states of the call */
+  int64_t row;         /* n >= 1: values of one state */
+  int64_t nslots;      /* slots of the cache */
+  int32_t block;       /* values that share a scale: 32, 64 or 128 (the last block may be short) */
+  int32_t format;      /* mamba2_code_format */
+  int32_t state_dtype; /* mamba2_dtype of the working states */
+} mamba2_state_cache_dims;
+
+/* Writes working state i (at state + i * state_row_stride elements, n values)
+ * into slot slots[i] of the cache.
+ *  slots   device int32 [b].  A negative slot skips the row; one >= nslots too,
+ *          and mamba2_device_errors reports bit 3.  Where several rows name one
+ *          slot, the last of them is written.
+ *  codes   [nslots, n] bytes; scales [nslots, ceil(n / block)] bytes.  Slots that
+ *          no row names are left as they were. */
+MAMBA2_API int mamba2_state_cache_store(const mamba2_state_cache_dims *dims, const void *state,
+                                        int64_t state_row_stride, const int32_t *slots,
+                                        void *codes, uint8_t *scales, void *stream);
+
+/* Reads slot slots[i] into working state i; rows with a negative slot (or one
+ * out of range, flagged as above) are left as they were.  Rows may share a slot. */
+MAMBA2_API int mamba2_state_cache_load(const mamba2_state_cache_dims *dims, const void *codes,
+                                       const uint8_t *scales, const int32_t *slots, void *state,
+                                       int64_t state_row_stride, void *stream);
 
 /* Profiling aid (no counterpart on the pages).  Arms the calling host thread
  * so that its NEXT call of mamba2_conv_ssd_prefill,

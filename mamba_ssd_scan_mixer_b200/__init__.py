@@ -11,6 +11,12 @@ Entry points (same names as the C ABI in include/mamba2ssd.h):
     mamba2_ssd_step(dims, params, xBC, z, dt_raw, y, conv_state, ssm_state, stream=None)
 Conveniences that allocate outputs and workspace with torch and call the above:
     prefill(...), step(...)
+
+Beside the mixer core:
+    gated_scan_prefill(...), gated_scan_step(...), gated_scan_backward(...)
+        the gated linear recurrence (one fp32 state a channel, decays from the token)
+    state_cache_store(...), state_cache_load(...)
+        recurrent states in slots of a cache of 8-bit codes
 """
 from __future__ import annotations
 
@@ -24,6 +30,10 @@ __all__ = [
     "step", "status_string", "mamba2_prefill_backward_workspace_size",
     "mamba2_conv_ssd_prefill_backward", "prefill_backward",
     "mamba2_prefill_host_workspace_size", "mamba2_conv_ssd_prefill_host", "prefill_host",
+    "Mamba2GatedScanDims", "GATED_SCAN_CHUNK", "make_gated_scan_dims",
+    "mamba2_gated_scan_workspace_size", "mamba2_gated_scan_backward_workspace_size",
+    "gated_scan_checkpoints", "gated_scan_prefill", "gated_scan_step", "gated_scan_backward",
+    "Mamba2StateCacheDims", "state_cache", "state_cache_store", "state_cache_load",
 ]
 
 MAMBA2_F32, MAMBA2_BF16 = 0, 1
@@ -46,6 +56,17 @@ class Mamba2Params(ctypes.Structure):
     _fields_ = [("conv_w", ctypes.c_void_p), ("conv_b", ctypes.c_void_p),
                 ("dt_bias", ctypes.c_void_p), ("A", ctypes.c_void_p), ("D", ctypes.c_void_p),
                 ("norm_w", ctypes.c_void_p)]
+
+
+class Mamba2GatedScanDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("width", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("decay_scale", ctypes.c_float)]
+
+
+class Mamba2StateCacheDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("row", ctypes.c_int64), ("nslots", ctypes.c_int64),
+                ("block", ctypes.c_int32), ("format", ctypes.c_int32),
+                ("state_dtype", ctypes.c_int32)]
 
 
 class Mamba2Error(RuntimeError):
@@ -101,6 +122,21 @@ def lib() -> ctypes.CDLL:
                                                        + [vp] * 15 + [vp, sz, vp])
         L.mamba2_ssd_step.restype = ctypes.c_int
         L.mamba2_ssd_step.argtypes = [pd, pp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp]
+        pg, pc = ctypes.POINTER(Mamba2GatedScanDims), ctypes.POINTER(Mamba2StateCacheDims)
+        for f in (L.mamba2_gated_scan_workspace_size, L.mamba2_gated_scan_backward_workspace_size,
+                  L.mamba2_gated_scan_checkpoint_count):
+            f.restype, f.argtypes = sz, [pg, ctypes.c_int]
+        rows4 = [vp, i64] * 4
+        L.mamba2_gated_scan_prefill.restype = ctypes.c_int
+        L.mamba2_gated_scan_prefill.argtypes = [pg, vp, *rows4, vp, vp, vp, i32, vp, vp, sz, vp]
+        L.mamba2_gated_scan_step.restype = ctypes.c_int
+        L.mamba2_gated_scan_step.argtypes = [pg, vp, *rows4, vp, vp, vp]
+        L.mamba2_gated_scan_backward.restype = ctypes.c_int
+        L.mamba2_gated_scan_backward.argtypes = [pg, vp, *rows4] + [vp] * 12 + [sz, vp]
+        L.mamba2_state_cache_store.restype = ctypes.c_int
+        L.mamba2_state_cache_store.argtypes = [pc, vp, i64, vp, vp, vp, vp]
+        L.mamba2_state_cache_load.restype = ctypes.c_int
+        L.mamba2_state_cache_load.argtypes = [pc, vp, vp, vp, vp, i64, vp]
         _lib = L
     return _lib
 
@@ -400,3 +436,281 @@ def prefill_backward(dims, params, xBC, z, dt_raw, dy, conv_state_in=None, ssm_s
     mamba2_conv_ssd_prefill_backward(dims, params, xBC, z, dt_raw, dy, grads, conv_state_in,
                                      ssm_state_in, d_ssm_state_out, workspace, stream)
     return grads
+
+
+# ---------------------------------------------------------------- gated scan
+
+#: Tokens of a checkpoint of the gated scan.
+GATED_SCAN_CHUNK = 128
+
+
+def make_gated_scan_dims(batch, seqlen, width, *, io_dtype="bf16",
+                         decay_scale=8.0) -> Mamba2GatedScanDims:
+    """Sizes of the gated scan.  Packed rows: batch = sequences, seqlen = all tokens."""
+    io = {"f32": MAMBA2_F32, "bf16": MAMBA2_BF16}.get(io_dtype, io_dtype)
+    return Mamba2GatedScanDims(int(batch), int(seqlen), int(width), int(io), float(decay_scale))
+
+
+def mamba2_gated_scan_workspace_size(dims: Mamba2GatedScanDims, packed: bool = False) -> int:
+    return int(lib().mamba2_gated_scan_workspace_size(ctypes.byref(dims), int(bool(packed))))
+
+
+def mamba2_gated_scan_backward_workspace_size(dims: Mamba2GatedScanDims,
+                                              packed: bool = False) -> int:
+    return int(lib().mamba2_gated_scan_backward_workspace_size(ctypes.byref(dims),
+                                                               int(bool(packed))))
+
+
+def gated_scan_checkpoints(dims: Mamba2GatedScanDims, packed: bool = False, device="cuda"):
+    """An fp32 tensor for the checkpoints of one prefill: [rows, ceil(L / 128), D]."""
+    import torch
+    rows = (1 if dims.seqlen > 0 else 0) if packed else dims.batch
+    return torch.empty(rows, -(-dims.seqlen // GATED_SCAN_CHUNK), dims.width,
+                       dtype=torch.float32, device=device)
+
+
+def _need(t, name, shape, dtype, device, contiguous=True):
+    if t.device != device or t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: {tuple(shape)} {dtype} on {device} expected, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def _row_stride(t, name):
+    """Elements from one token to the next of [..., tokens, D] rows that follow one another."""
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name}: last dimension must be contiguous")
+    if t.dim() == 2:
+        return st[0] if t.shape[0] > 1 else max(st[0], t.shape[1])
+    b, n = t.shape[0], t.shape[1]
+    rs = st[1] if n > 1 else (st[0] if b > 1 else max(st[1], t.shape[2]))
+    if b > 1 and n > 1 and st[0] != n * rs:
+        raise ValueError(f"{name}: batch stride must be rows * row stride")
+    return rs
+
+
+def _gs_io(dims):
+    import torch
+    if dims.io_dtype not in (MAMBA2_F32, MAMBA2_BF16):
+        raise ValueError("io_dtype: f32 or bf16")
+    return torch.float32 if dims.io_dtype == MAMBA2_F32 else torch.bfloat16
+
+
+def _gs_inputs(dims, shape, lam, x, r, g, z):
+    """The shared inputs checked: their device, dtype and (pointer, row stride) arguments."""
+    import torch
+    dt, dev = _gs_io(dims), x.device
+    if dev.type != "cuda":
+        raise ValueError(f"x: a CUDA tensor expected, got {dev}")
+    _need(lam, "lam", (dims.width,), torch.float32, dev)
+    rows = []
+    for name, t in (("x", x), ("r", r), ("g", g), ("z", z)):
+        if t is None and name == "z":
+            rows += [None, 0]
+            continue
+        _need(t, name, shape, dt, dev, contiguous=False)
+        rows += [t.data_ptr(), _row_stride(t, name)]
+    return dev, dt, rows
+
+
+class _On:
+    """A call's surroundings: the tensors' device current and, where the caller names a stream,
+    that stream too, so that what the call allocates belongs to the stream it is used on."""
+
+    def __init__(self, dev, stream):
+        import torch
+        self.other = None
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = (torch.cuda.ExternalStream(int(stream), dev) if int(stream)
+                          else torch.cuda.default_stream(dev))
+            if stream.device != dev:
+                raise ValueError(f"stream: one of {dev} expected, got one of {stream.device}")
+            self.other = torch.cuda.stream(stream)
+            self.stream = stream.cuda_stream
+        else:
+            if torch.cuda.current_device() != dev.index:
+                self.other = torch.cuda.device(dev)
+            self.stream = torch.cuda.current_stream(dev).cuda_stream
+
+    def __enter__(self):
+        if self.other is not None:
+            self.other.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.other is not None:
+            self.other.__exit__(*exc)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(workspace, size, dev):
+    """The caller's workspace, or a new one: (tensor, address, bytes)."""
+    import torch
+    if workspace is None:
+        workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on {dev} expected")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _gs_optional(dims, packed, cu_seqlens, states, checkpoints, dev):
+    import torch
+    if packed:
+        _need(cu_seqlens, "cu_seqlens", (dims.batch + 1,), torch.int32, dev)
+    for name, t in states:
+        if t is not None:
+            _need(t, name, (dims.batch, dims.width), torch.float32, dev)
+    if checkpoints is not None:
+        rows = (1 if dims.seqlen > 0 else 0) if packed else dims.batch
+        _need(checkpoints, "checkpoints", (rows, -(-dims.seqlen // GATED_SCAN_CHUNK), dims.width),
+              torch.float32, dev)
+
+
+def gated_scan_prefill(dims, lam, x, r, g, z=None, h_state=None, states_in=False, cu_seqlens=None,
+                       checkpoints=None, workspace=None, y=None, stream=None):
+    """The gated linear recurrence over dims.seqlen tokens (mamba2_gated_scan_prefill).
+
+    x, r, g and z (optional output gate) [b, L, D], or [T, D] with cu_seqlens (CUDA int32
+    [b + 1]); views with unit last stride, e.g. columns of one projection.  lam [D] fp32.
+    h_state [b, D] fp32 (optional) holds the initial states when states_in is true and
+    receives the final ones.  checkpoints: see gated_scan_checkpoints, for the backward
+    pass.  Allocates y (and the workspace) if not given; returns y."""
+    import torch
+    packed = cu_seqlens is not None
+    shape = (dims.seqlen, dims.width) if packed else (dims.batch, dims.seqlen, dims.width)
+    dev, dt, rows = _gs_inputs(dims, shape, lam, x, r, g, z)
+    _gs_optional(dims, packed, cu_seqlens, (("h_state", h_state),), checkpoints, dev)
+    if y is not None:
+        _need(y, "y", shape, dt, dev)
+    with _On(dev, stream) as s:
+        if y is None:
+            y = torch.empty(shape, dtype=dt, device=dev)
+        ws, ws_at, ws_bytes = _scratch(workspace, mamba2_gated_scan_workspace_size(dims, packed),
+                                       dev)
+        st = lib().mamba2_gated_scan_prefill(
+            ctypes.byref(dims), lam.data_ptr(), *rows, _addr(cu_seqlens), y.data_ptr(),
+            _addr(h_state), int(bool(states_in)), _addr(checkpoints), ws_at, ws_bytes, s)
+    if st != 0:
+        raise Mamba2Error(st, "mamba2_gated_scan_prefill")
+    return y
+
+
+def gated_scan_step(dims, lam, x, r, g, h_state, z=None, y=None, stream=None):
+    """One token of every sequence: x, r, g, z [b, D]; h_state [b, D] fp32 is updated in
+    place.  Allocates y [b, D] if not given and returns it."""
+    import torch
+    shape = (dims.batch, dims.width)
+    dev, dt, rows = _gs_inputs(dims, shape, lam, x, r, g, z)
+    _need(h_state, "h_state", shape, torch.float32, dev)
+    if y is not None:
+        _need(y, "y", shape, dt, dev)
+    with _On(dev, stream) as s:
+        if y is None:
+            y = torch.empty(shape, dtype=dt, device=dev)
+        st = lib().mamba2_gated_scan_step(ctypes.byref(dims), lam.data_ptr(), *rows, y.data_ptr(),
+                                          h_state.data_ptr(), s)
+    if st != 0:
+        raise Mamba2Error(st, "mamba2_gated_scan_step")
+    return y
+
+
+def gated_scan_backward(dims, lam, x, r, g, dy, z=None, h_state_in=None, d_h_state_out=None,
+                        cu_seqlens=None, checkpoints=None, workspace=None, stream=None):
+    """Gradients of sum(y dy) + sum(final state d_h_state_out) of gated_scan_prefill.
+
+    Inputs as for the prefill; dy contiguous like y; h_state_in the state it began with (None:
+    zero); checkpoints: those it wrote (None: the scan is run again).  Returns a dict "x",
+    "r", "g", "lam", with z "z", and with h_state_in "h_state"."""
+    import torch
+    packed = cu_seqlens is not None
+    shape = (dims.seqlen, dims.width) if packed else (dims.batch, dims.seqlen, dims.width)
+    dev, dt, rows = _gs_inputs(dims, shape, lam, x, r, g, z)
+    _need(dy, "dy", shape, dt, dev)
+    _gs_optional(dims, packed, cu_seqlens,
+                 (("h_state_in", h_state_in), ("d_h_state_out", d_h_state_out)), checkpoints, dev)
+    with _On(dev, stream) as s:
+        grads = {k: torch.empty(shape, dtype=dt, device=dev)
+                 for k in (("x", "r", "g") if z is None else ("x", "r", "g", "z"))}
+        grads["lam"] = torch.empty(dims.width, dtype=torch.float32, device=dev)
+        if h_state_in is not None:
+            grads["h_state"] = torch.empty(dims.batch, dims.width, dtype=torch.float32, device=dev)
+        ws, ws_at, ws_bytes = _scratch(
+            workspace, mamba2_gated_scan_backward_workspace_size(dims, packed), dev)
+        st = lib().mamba2_gated_scan_backward(
+            ctypes.byref(dims), lam.data_ptr(), *rows, _addr(cu_seqlens), _addr(h_state_in),
+            dy.data_ptr(), _addr(d_h_state_out), _addr(checkpoints), grads["x"].data_ptr(),
+            grads["r"].data_ptr(), grads["g"].data_ptr(), _addr(grads.get("z")),
+            grads["lam"].data_ptr(), _addr(grads.get("h_state")), ws_at, ws_bytes, s)
+    if st != 0:
+        raise Mamba2Error(st, "mamba2_gated_scan_backward")
+    return grads
+
+
+# ---------------------------------------------------------------- state cache
+
+_CODES = ("int8", "e4m3")  # mamba2_code_format
+
+
+def state_cache(nslots, row, block=64, codes="int8", device="cuda"):
+    """An empty cache for `nslots` states of `row` values: (codes [nslots, row] int8 or
+    float8_e4m3fn, scales [nslots, ceil(row / block)] uint8), all zero."""
+    import torch
+    if codes not in _CODES:
+        raise ValueError("codes: int8 or e4m3")
+    dt = torch.int8 if codes == "int8" else torch.float8_e4m3fn
+    return (torch.zeros(nslots, row, dtype=dt, device=device),
+            torch.zeros(nslots, -(-row // block), dtype=torch.uint8, device=device))
+
+
+def _state_cache_args(state, slots, codes, scales, block):
+    import torch
+    dev = state.device
+    if dev.type != "cuda":
+        raise ValueError(f"state: a CUDA tensor expected, got {dev}")
+    if state.dim() < 2 or state.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("state: [b, ...] of fp32 or bf16 expected")
+    if codes.dim() != 2 or codes.dtype not in (torch.int8, torch.float8_e4m3fn):
+        raise ValueError("codes: [slots, row] of int8 or float8_e4m3fn expected")
+    b, (nslots, row) = state.shape[0], codes.shape
+    if state.numel() != b * row:
+        raise ValueError(f"state: {row} values a row expected, got {tuple(state.shape)}")
+    if b and not state[0].is_contiguous():
+        raise ValueError("state: each row's values must be contiguous")
+    if block not in (32, 64, 128):
+        raise ValueError("block: 32, 64 or 128")
+    _need(slots, "slots", (b,), torch.int32, dev)
+    _need(codes, "codes", codes.shape, codes.dtype, dev)
+    _need(scales, "scales", (nslots, -(-row // block)), torch.uint8, dev)
+    dims = Mamba2StateCacheDims(b, row, nslots, int(block), int(codes.dtype != torch.int8),
+                                MAMBA2_F32 if state.dtype == torch.float32 else MAMBA2_BF16)
+    return dev, dims, state.stride(0) if b > 1 else row
+
+
+def state_cache_store(state, slots, codes, scales, block=64, stream=None) -> None:
+    """Write working states [b, ...] (fp32 or bf16) into slots (CUDA int32 [b]; negative:
+    skipped; the last row of those that name one slot counts) of a cache (see state_cache)."""
+    dev, dims, ld = _state_cache_args(state, slots, codes, scales, block)
+    with _On(dev, stream) as s:
+        st = lib().mamba2_state_cache_store(ctypes.byref(dims), state.data_ptr(), ld,
+                                            slots.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                            s)
+    if st != 0:
+        raise Mamba2Error(st, "mamba2_state_cache_store")
+
+
+def state_cache_load(codes, scales, slots, state, block=64, stream=None) -> None:
+    """Read slots of a cache into working states [b, ...]; rows with a negative slot are left
+    as they were."""
+    dev, dims, ld = _state_cache_args(state, slots, codes, scales, block)
+    with _On(dev, stream) as s:
+        st = lib().mamba2_state_cache_load(ctypes.byref(dims), codes.data_ptr(),
+                                           scales.data_ptr(), slots.data_ptr(), state.data_ptr(),
+                                           ld, s)
+    if st != 0:
+        raise Mamba2Error(st, "mamba2_state_cache_load")

@@ -8,6 +8,8 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "gated_scan.cuh"
+#include "state_cache.cuh"
 
 namespace m2 {
 namespace {
@@ -155,6 +157,10 @@ MAMBA2_API int mamba2_device_errors(unsigned int *flags) {
   if (take_step_errors(&f) != cudaSuccess) return MAMBA2_ERR_CUDA;
   *flags |= f;
   if (take_prefill_tc_errors(&f) != cudaSuccess) return MAMBA2_ERR_CUDA;
+  *flags |= f;
+  if (take_gated_scan_errors(&f) != cudaSuccess) return MAMBA2_ERR_CUDA;
+  *flags |= f;
+  if (take_state_cache_errors(&f) != cudaSuccess) return MAMBA2_ERR_CUDA;
   *flags |= f;
   return MAMBA2_OK;
 }
@@ -661,6 +667,257 @@ MAMBA2_API int mamba2_conv_ssd_prefill_backward(
   a.ws = static_cast<char *>(workspace);
   a.stream = static_cast<cudaStream_t>(stream);
   return prefill_backward(a) == cudaSuccess ? MAMBA2_OK : MAMBA2_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- gated scan
+namespace m2 {
+namespace {
+
+int gated_scan_dims_status(const mamba2_gated_scan_dims *d) {
+  if (d == nullptr || d->batch < 0 || d->seqlen < 0 || d->width < 1) return MAMBA2_ERR_INVALID_ARG;
+  if (d->io_dtype != MAMBA2_F32 && d->io_dtype != MAMBA2_BF16) return MAMBA2_ERR_INVALID_ARG;
+  if (!(d->decay_scale > 0.0f) || !std::isfinite(d->decay_scale)) return MAMBA2_ERR_INVALID_ARG;
+  if (d->width % 8 != 0 || d->width > (1 << 20)) return MAMBA2_ERR_UNSUPPORTED;
+  // tokens and chunks are counted in 32 bits
+  if (d->batch >= (int64_t)1 << 31 || d->seqlen >= (int64_t)1 << 31 ||
+      d->batch * ceil_div(std::max<int64_t>(d->seqlen, 1), kGsChunk) >= (int64_t)1 << 31)
+    return MAMBA2_ERR_UNSUPPORTED;
+  return MAMBA2_OK;
+}
+
+int64_t gated_scan_rows(const mamba2_gated_scan_dims *d, bool packed) {
+  return packed ? (d->seqlen > 0 ? 1 : 0) : d->batch;
+}
+
+bool rows_ok(const void *p, int64_t ld, int64_t width) {
+  return p != nullptr && aligned(p, 16) && ld >= width && ld % 8 == 0;
+}
+
+// The inputs shared by prefill, step and backward.
+int gated_scan_inputs(const mamba2_gated_scan_dims *d, const float *lam, const void *x,
+                      int64_t ld_x, const void *r, int64_t ld_r, const void *g, int64_t ld_g,
+                      const void *z, int64_t ld_z, bool tokens, GatedScanArgs *a) {
+  const int st = gated_scan_dims_status(d);
+  if (st != MAMBA2_OK) return st;
+  if (lam == nullptr || !aligned(lam, 4)) return MAMBA2_ERR_INVALID_ARG;
+  if (tokens && (!rows_ok(x, ld_x, d->width) || !rows_ok(r, ld_r, d->width) ||
+                 !rows_ok(g, ld_g, d->width) || (z != nullptr && !rows_ok(z, ld_z, d->width))))
+    return MAMBA2_ERR_INVALID_ARG;
+  a->batch = d->batch;
+  a->L = d->seqlen;
+  a->D = d->width;
+  a->io = d->io_dtype;
+  a->c = d->decay_scale;
+  a->lam = lam;
+  a->x = x;
+  a->r = r;
+  a->g = g;
+  a->z = z;
+  a->ld_x = ld_x;
+  a->ld_r = ld_r;
+  a->ld_g = ld_g;
+  a->ld_z = ld_z;
+  return MAMBA2_OK;
+}
+
+}  // namespace
+}  // namespace m2
+
+MAMBA2_API size_t mamba2_gated_scan_workspace_size(const mamba2_gated_scan_dims *dims,
+                                                   int packed) {
+  if (gated_scan_dims_status(dims) != MAMBA2_OK) return 0;
+  return gated_scan_workspace(gated_scan_rows(dims, packed != 0), dims->seqlen, dims->width,
+                              dims->batch, packed != 0);
+}
+
+MAMBA2_API size_t mamba2_gated_scan_backward_workspace_size(const mamba2_gated_scan_dims *dims,
+                                                            int packed) {
+  if (gated_scan_dims_status(dims) != MAMBA2_OK) return 0;
+  return gated_scan_backward_workspace(gated_scan_rows(dims, packed != 0), dims->seqlen,
+                                       dims->width, dims->batch, packed != 0);
+}
+
+MAMBA2_API size_t mamba2_gated_scan_checkpoint_count(const mamba2_gated_scan_dims *dims,
+                                                     int packed) {
+  if (gated_scan_dims_status(dims) != MAMBA2_OK) return 0;
+  return (size_t)gated_scan_rows(dims, packed != 0) * (size_t)ceil_div(dims->seqlen, kGsChunk) *
+         (size_t)dims->width;
+}
+
+MAMBA2_API int mamba2_gated_scan_prefill(
+    const mamba2_gated_scan_dims *dims, const float *lam, const void *x, int64_t x_row_stride,
+    const void *r, int64_t r_row_stride, const void *g, int64_t g_row_stride, const void *z,
+    int64_t z_row_stride, const int32_t *cu_seqlens, void *y, float *h_state, int32_t states_in,
+    float *checkpoints, void *workspace, size_t workspace_bytes, void *stream) {
+  NvtxRange range("mamba2_gated_scan_prefill");
+  GatedScanArgs a;
+  const bool tokens = dims != nullptr && dims->seqlen > 0 && (dims->batch > 0 || cu_seqlens);
+  const int st = gated_scan_inputs(dims, lam, x, x_row_stride, r, r_row_stride, g, g_row_stride, z,
+                                   z_row_stride, tokens, &a);
+  if (st != MAMBA2_OK) return st;
+  if (states_in != 0 && states_in != 1) return MAMBA2_ERR_INVALID_ARG;
+  if ((states_in && h_state == nullptr) || !aligned(h_state, 16) || !aligned(checkpoints, 16) ||
+      !aligned(cu_seqlens, 4))
+    return MAMBA2_ERR_INVALID_ARG;
+  if (cu_seqlens != nullptr && dims->batch == 0 && dims->seqlen > 0) return MAMBA2_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!tokens) {  // the states pass through, or start (and stay) at zero
+    if (!states_in && h_state != nullptr && dims->batch > 0 &&
+        cudaMemsetAsync(h_state, 0, (size_t)dims->batch * dims->width * 4, s) != cudaSuccess)
+      return MAMBA2_ERR_CUDA;
+    return MAMBA2_OK;
+  }
+  if (y == nullptr || !aligned(y, 16)) return MAMBA2_ERR_INVALID_ARG;
+  const bool packed = cu_seqlens != nullptr;
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < mamba2_gated_scan_workspace_size(dims, packed))
+    return MAMBA2_ERR_WORKSPACE;
+  a.cu = cu_seqlens;
+  a.y = y;
+  a.h = h_state;
+  a.states_in = states_in;
+  a.ck = checkpoints;
+  a.ws = static_cast<char *>(workspace);
+  a.stream = s;
+  return gated_scan_prefill(a) == cudaSuccess ? MAMBA2_OK : MAMBA2_ERR_CUDA;
+}
+
+MAMBA2_API int mamba2_gated_scan_step(const mamba2_gated_scan_dims *dims, const float *lam,
+                                      const void *x, int64_t x_row_stride, const void *r,
+                                      int64_t r_row_stride, const void *g, int64_t g_row_stride,
+                                      const void *z, int64_t z_row_stride, void *y, float *h_state,
+                                      void *stream) {
+  NvtxRange range("mamba2_gated_scan_step");
+  GatedScanArgs a;
+  mamba2_gated_scan_dims d = {};
+  if (dims == nullptr) return MAMBA2_ERR_INVALID_ARG;
+  d = *dims;
+  d.seqlen = 1;
+  const int st = gated_scan_inputs(&d, lam, x, x_row_stride, r, r_row_stride, g, g_row_stride, z,
+                                   z_row_stride, d.batch > 0, &a);
+  if (st != MAMBA2_OK) return st;
+  if (d.batch == 0) return MAMBA2_OK;
+  if (y == nullptr || !aligned(y, 16) || h_state == nullptr || !aligned(h_state, 16))
+    return MAMBA2_ERR_INVALID_ARG;
+  a.cu = nullptr;
+  a.y = y;
+  a.h = h_state;
+  a.states_in = 1;
+  a.ws = nullptr;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return gated_scan_step(a) == cudaSuccess ? MAMBA2_OK : MAMBA2_ERR_CUDA;
+}
+
+MAMBA2_API int mamba2_gated_scan_backward(
+    const mamba2_gated_scan_dims *dims, const float *lam, const void *x, int64_t x_row_stride,
+    const void *r, int64_t r_row_stride, const void *g, int64_t g_row_stride, const void *z,
+    int64_t z_row_stride, const int32_t *cu_seqlens, const float *h_state_in, const void *dy,
+    const float *d_h_state_out, const float *checkpoints, void *d_x, void *d_r, void *d_g,
+    void *d_z, float *d_lam, float *d_h_state_in, void *workspace, size_t workspace_bytes,
+    void *stream) {
+  NvtxRange range("mamba2_gated_scan_backward");
+  GatedScanBackwardArgs b;
+  const bool tokens = dims != nullptr && dims->seqlen > 0 && (dims->batch > 0 || cu_seqlens);
+  const int st = gated_scan_inputs(dims, lam, x, x_row_stride, r, r_row_stride, g, g_row_stride, z,
+                                   z_row_stride, tokens, &b.f);
+  if (st != MAMBA2_OK) return st;
+  if (d_lam == nullptr || !aligned(d_lam, 4) || !aligned(h_state_in, 16) ||
+      !aligned(d_h_state_out, 16) || !aligned(d_h_state_in, 16) || !aligned(checkpoints, 16) ||
+      !aligned(cu_seqlens, 4))
+    return MAMBA2_ERR_INVALID_ARG;
+  if (cu_seqlens != nullptr && dims->batch == 0 && dims->seqlen > 0) return MAMBA2_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!tokens) {  // the state's gradient passes through
+    const size_t bytes = (size_t)dims->batch * dims->width * 4;
+    cudaError_t e = cudaMemsetAsync(d_lam, 0, (size_t)dims->width * 4, s);
+    if (e == cudaSuccess && d_h_state_in != nullptr && bytes > 0)
+      e = d_h_state_out != nullptr ? cudaMemcpyAsync(d_h_state_in, d_h_state_out, bytes,
+                                                     cudaMemcpyDeviceToDevice, s)
+                                   : cudaMemsetAsync(d_h_state_in, 0, bytes, s);
+    return e == cudaSuccess ? MAMBA2_OK : MAMBA2_ERR_CUDA;
+  }
+  const void *rows[] = {dy, d_x, d_r, d_g};
+  for (const void *p : rows)
+    if (p == nullptr || !aligned(p, 16)) return MAMBA2_ERR_INVALID_ARG;
+  if ((z != nullptr) != (d_z != nullptr) || !aligned(d_z, 16)) return MAMBA2_ERR_INVALID_ARG;
+  const bool packed = cu_seqlens != nullptr;
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < mamba2_gated_scan_backward_workspace_size(dims, packed))
+    return MAMBA2_ERR_WORKSPACE;
+  b.f.cu = cu_seqlens;
+  b.f.y = nullptr;
+  b.f.h = nullptr;
+  b.f.states_in = 0;
+  b.f.ws = static_cast<char *>(workspace);
+  b.f.stream = s;
+  b.h_in = h_state_in;
+  b.dy = dy;
+  b.dh = d_h_state_out;
+  b.ck = checkpoints;
+  b.dx = d_x;
+  b.dr = d_r;
+  b.dg = d_g;
+  b.dz = d_z;
+  b.dlam = d_lam;
+  b.dh_in = d_h_state_in;
+  return gated_scan_backward(b) == cudaSuccess ? MAMBA2_OK : MAMBA2_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- state cache
+namespace m2 {
+namespace {
+
+// MAMBA2_OK, an error, or 1 where there is nothing to do.
+int state_cache_args(const mamba2_state_cache_dims *d, const void *state, int64_t ld,
+                     const int32_t *slots, const void *codes, const uint8_t *scales, void *stream,
+                     StateCacheArgs *a) {
+  if (d == nullptr || d->batch < 0 || d->row < 1 || d->nslots < 0) return MAMBA2_ERR_INVALID_ARG;
+  if (d->format != MAMBA2_CODES_INT8 && d->format != MAMBA2_CODES_E4M3)
+    return MAMBA2_ERR_INVALID_ARG;
+  if (d->state_dtype != MAMBA2_F32 && d->state_dtype != MAMBA2_BF16) return MAMBA2_ERR_INVALID_ARG;
+  if (d->block != 32 && d->block != 64 && d->block != 128) return MAMBA2_ERR_UNSUPPORTED;
+  // grid limits
+  if (d->batch > 65535 || d->row >= (int64_t)1 << 36) return MAMBA2_ERR_UNSUPPORTED;
+  if (d->batch == 0) return 1;
+  if (state == nullptr || slots == nullptr || codes == nullptr || scales == nullptr ||
+      ld < d->row || !aligned(state, d->state_dtype == MAMBA2_BF16 ? 2 : 4) || !aligned(slots, 4))
+    return MAMBA2_ERR_INVALID_ARG;
+  a->batch = d->batch;
+  a->n = d->row;
+  a->nslots = d->nslots;
+  a->block = d->block;
+  a->format = d->format;
+  a->state_dtype = d->state_dtype;
+  a->state = const_cast<void *>(state);
+  a->ld = ld;
+  a->slots = slots;
+  a->codes = const_cast<void *>(codes);
+  a->scales = const_cast<uint8_t *>(scales);
+  a->stream = static_cast<cudaStream_t>(stream);
+  return MAMBA2_OK;
+}
+
+}  // namespace
+}  // namespace m2
+
+MAMBA2_API int mamba2_state_cache_store(const mamba2_state_cache_dims *dims, const void *state,
+                                        int64_t state_row_stride, const int32_t *slots,
+                                        void *codes, uint8_t *scales, void *stream) {
+  NvtxRange range("mamba2_state_cache_store");
+  StateCacheArgs a;
+  const int st = state_cache_args(dims, state, state_row_stride, slots, codes, scales, stream, &a);
+  if (st != MAMBA2_OK) return st < 0 ? st : MAMBA2_OK;
+  return state_cache_store(a) == cudaSuccess ? MAMBA2_OK : MAMBA2_ERR_CUDA;
+}
+
+MAMBA2_API int mamba2_state_cache_load(const mamba2_state_cache_dims *dims, const void *codes,
+                                       const uint8_t *scales, const int32_t *slots, void *state,
+                                       int64_t state_row_stride, void *stream) {
+  NvtxRange range("mamba2_state_cache_load");
+  StateCacheArgs a;
+  const int st = state_cache_args(dims, state, state_row_stride, slots, codes, scales, stream, &a);
+  if (st != MAMBA2_OK) return st < 0 ? st : MAMBA2_OK;
+  return state_cache_load(a) == cudaSuccess ? MAMBA2_OK : MAMBA2_ERR_CUDA;
 }
 
 }  // extern "C"

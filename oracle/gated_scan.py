@@ -1,0 +1,105 @@
+"""fp64 oracle of the gated linear recurrence (test infrastructure, no library code).
+
+One sequence, token by token:
+    s = softplus(lam)   R = sigmoid(r)   G = sigmoid(g)   la = -c s R
+    a = exp(la)   m = sqrt(1 - a^2)   h_t = a h_{t-1} + m G x_t   y_t = h_t [silu(z_t)]
+and the gradients of sum(y dy) + sum(h_L dh) by the reverse recurrence
+    d_t = dy_t silu(z_t) + a_{t+1} d_{t+1}.
+
+`bounds` gives, beside each result, how far a computation in fp32 may be off: every
+factor that enters a product is taken to be off by KAPPA half-steps of fp32, and the
+recurrences carry those errors on, over the magnitudes (absolute sums, so that
+cancellation is covered).  KAPPA: the argument of sigmoid's exponential is off by
+half a step of |r| <= 8, the exponential, the sum and the quotient by one or two
+steps each (|r| + 5); la and a add four and m, a square root, halves what it is
+given; b = m G x has two such factors, and three products: 2 * 13 + 3 < 32.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+U = 2.0 ** -24  # half a step of fp32
+KAPPA = 32
+
+
+def _sigmoid(v):
+    with np.errstate(over="ignore"):
+        return 1.0 / (1.0 + np.exp(-v))
+
+
+def _gates(lam, r, g, c):
+    s = np.logaddexp(0.0, lam)
+    R, G = _sigmoid(r), _sigmoid(g)
+    la = -c * s * R
+    return R, G, la, np.exp(la), np.sqrt(-np.expm1(2.0 * la))
+
+
+def forward(lam, x, r, g, z=None, h0=None, c=8.0):
+    """One sequence: x, r, g, z [L, D], lam, h0 [D].  A dict: y, h (all states [L, D]),
+    h_end, and the bounds y_off, h_off, h_end_off, with `size` the magnitudes."""
+    L, D = x.shape
+    R, G, la, a, m = _gates(lam, r, g, c)
+    b = m * G * x
+    h = np.zeros(D) if h0 is None else h0.astype(np.float64)
+    hs, size, off = np.empty((L, D)), np.empty((L, D)), np.empty((L, D))
+    M, E = np.abs(h), np.zeros(D)
+    for t in range(L):
+        h = a[t] * h + b[t]
+        M = a[t] * M + np.abs(b[t])
+        E = a[t] * E + KAPPA * U * M
+        hs[t], size[t], off[t] = h, M, E
+    out = {"h": hs, "h_end": h, "size": size, "h_off": off, "h_end_off": E}
+    if z is None:
+        out["y"], out["y_off"] = hs, off
+    else:
+        gate = z * _sigmoid(z)
+        out["y"] = hs * gate
+        out["y_off"] = (off + KAPPA * U * size) * np.abs(gate)
+    return out
+
+
+def backward(lam, x, r, g, dy, z=None, h0=None, dh=None, c=8.0):
+    """The gradients x, r, g, lam, h0 (and z), each with its bound as "<name>_off"."""
+    L, D = x.shape
+    R, G, la, a, m = _gates(lam, r, g, c)
+    f = forward(lam, x, r, g, None, h0, c)
+    h, size, off = f["h"], f["size"], f["h_off"]
+    start = np.zeros(D) if h0 is None else h0.astype(np.float64)
+    hp = np.concatenate([start[None], h[:-1]]) if L else h
+    hp_size = np.concatenate([np.abs(start)[None], size[:-1]]) if L else h
+    hp_off = np.concatenate([np.zeros((1, D)), off[:-1]]) if L else h
+    out = {}
+    ds = dy.astype(np.float64)
+    if z is not None:
+        sig = _sigmoid(z)
+        slope = sig * (1.0 + z * (1.0 - sig))
+        out["z"] = dy * h * slope
+        # 1 + z (1 - sig) cancels for negative z: its error goes by 1 + |z| (1 - sig)
+        wide = sig * (1.0 + np.abs(z) * (1.0 - sig))
+        out["z_off"] = np.abs(dy) * (off * wide + KAPPA * U * size * wide)
+        ds = dy * z * sig
+    e = np.zeros(D) if dh is None else dh.astype(np.float64)
+    eM, eE = np.abs(e), np.zeros(D)
+    d, dM, dE = np.empty((L, D)), np.empty((L, D)), np.empty((L, D))
+    for t in range(L - 1, -1, -1):
+        d[t] = ds[t] + e
+        dM[t] = np.abs(ds[t]) + eM
+        dE[t] = eE + KAPPA * U * dM[t]
+        e, eM, eE = a[t] * d[t], a[t] * dM[t], a[t] * (dE[t] + KAPPA * U * dM[t])
+    out["h0"], out["h0_off"] = e, eE
+    out["x"], out["x_off"] = d * m * G, m * G * (dE + KAPPA * U * dM)
+    out["g"] = d * m * x * G * (1.0 - G)
+    # 1 - G: half a step of one beside its own size
+    out["g_off"] = m * np.abs(x) * G * ((1.0 - G) * (dE + KAPPA * U * dM) + KAPPA * U * dM)
+    per_m = np.where(m > 0, 1.0 / np.where(m > 0, m, 1.0), 0.0)
+    k = a * hp - a * a * per_m * G * x
+    k_size = a * hp_size + a * a * per_m * G * np.abs(x)
+    dla = d * k
+    dla_off = dE * k_size + dM * (a * hp_off + 2 * KAPPA * U * k_size)
+    out["r"] = dla * la * (1.0 - R)
+    out["r_off"] = np.abs(la) * ((1.0 - R) * dla_off + KAPPA * U * dM * k_size)
+    sl = c * _sigmoid(lam)
+    out["lam"] = -sl * (dla * R).sum(0)
+    # the terms' errors, and those of summing 128 tokens and then the pieces
+    out["lam_off"] = sl * (R * (dla_off + (KAPPA + 128 + L / 128) * U * dM * k_size)).sum(0)
+    return out
