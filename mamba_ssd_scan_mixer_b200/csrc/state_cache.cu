@@ -32,76 +32,302 @@ template <bool INT8> __device__ __forceinline__ int scale_byte(float amax) {
 __device__ __forceinline__ float inverse_of(int byte) {
   return __int_as_float((254 - byte) << 23);
 }
-template <bool INT8> __device__ __forceinline__ uint8_t encode(float v) {
-  if (INT8) return (uint8_t)(int8_t)__float2int_rn(v);
-  return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+
+// Four values times 2^-e (exact) as four codes, the first in the low byte.
+template <bool INT8> __device__ __forceinline__ uint32_t encode4(const float *v, float inv) {
+  if (INT8) {
+    // adding 1.5 2^23 rounds to an integer (to nearest, ties to even) and leaves it
+    // in the low bits
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(fmaf(v[i], inv, 12582912.0f));
+    return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+  }
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv),
+                                               __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv),
+                                               __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
 }
-template <bool INT8> __device__ __forceinline__ float decode(uint8_t q) {
-  if (INT8) return (float)(int8_t)q;
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3)));
+template <bool INT8> __device__ __forceinline__ uint32_t encode1(float v, float inv) {
+  if (INT8) return __float_as_uint(fmaf(v, inv, 12582912.0f)) & 0xffu;
+  return __nv_cvt_float_to_fp8(v * inv, __NV_SATFINITE, __NV_E4M3);
+}
+template <bool INT8>
+__device__ __forceinline__ void decode4(uint32_t q, float scale, float *v) {
+  if (INT8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(q >> (8 * i)) * scale;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 f = __half22float2(
+          __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q >> (16 * i)), __NV_E4M3)));
+      v[2 * i] = f.x * scale;
+      v[2 * i + 1] = f.y * scale;
+    }
+  }
+}
+template <bool INT8> __device__ __forceinline__ float decode1(uint32_t q, float scale) {
+  if (INT8) return (float)(int8_t)q * scale;
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)q, __NV_E4M3))) * scale;
+}
+// The scale to decode with; NaN for a block that held something not finite.
+__device__ __forceinline__ float scale_of(int byte) {
+  return byte == 255 ? __int_as_float(0x7fffffff) : pow2_of(byte);
 }
 
 // The slot of batch row b, or -1 if nothing is to be done for it: a negative
-// slot, one out of range (flagged), or (store) one that a later row names too.
+// slot, or one out of range (flagged).
 __device__ __forceinline__ int64_t slot_of(const int32_t *slots, int64_t b, int64_t nslots) {
   const int64_t s = slots[b];
   if (s >= nslots) {
-    atomicOr(&g_sc_errors, kErrSlots);
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_sc_errors, kErrSlots);
     return -1;
   }
   return s < 0 ? -1 : s;
 }
-
-template <typename T, bool INT8>
-__global__ void store_kernel(const T *state, int64_t ld, int64_t n, int block, int64_t nb,
-                             const int32_t *slots, int64_t batch, int64_t nslots, uint8_t *codes,
-                             uint8_t *scales) {
-  const int64_t b = blockIdx.y;
-  const int64_t s = slot_of(slots, b, nslots);
-  if (s < 0) return;
+// Whether a later row names slot s too (then this row is not written).  Each block
+// reads the rest of the slots: 4 bytes a row, small beside a state of thousands of
+// values for batches of the usual size.
+__device__ __forceinline__ bool named_later(const int32_t *slots, int64_t b, int64_t batch,
+                                            int64_t s) {
   int later = 0;
   for (int64_t i = b + 1 + threadIdx.x; i < batch; i += blockDim.x) later |= slots[i] == s;
-  if (__syncthreads_or(later)) return;
-  const int64_t k = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+  return __syncthreads_or(later) != 0;
+}
+
+constexpr int kThreads = 256;
+
+// 16 bytes of a state: V = 4 or 8 values.
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+  static constexpr int V = 4;
+  static __device__ __forceinline__ void get(uint4 u, float *v) {
+    v[0] = __uint_as_float(u.x), v[1] = __uint_as_float(u.y);
+    v[2] = __uint_as_float(u.z), v[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 put(const float *v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+  }
+};
+template <> struct Vec<__nv_bfloat16> {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ void get(uint4 u, float *v) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 put(const float *v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 q = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&q);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// Rows on 16-byte boundaries: a lane takes 16 bytes of the state, LANES lanes a
+// block of LANES * V values; a warp has kU such pieces of 32 * V values under way.
+constexpr int kU = 4;
+template <typename T, bool INT8, int LANES>
+__global__ void __launch_bounds__(kThreads)
+    store_vec_kernel(const T *__restrict__ state, int64_t ld, int64_t n, int64_t nb,
+                     const int32_t *__restrict__ slots, int64_t batch, int64_t nslots,
+                     uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+  constexpr int V = Vec<T>::V;
+  const int64_t b = blockIdx.y;
   const int lane = threadIdx.x & 31;
-  if (k >= nb) return;
-  const int64_t i0 = k * block, i1 = min(n, i0 + block);
-  int m = 0;  // the largest magnitude as bits: an order that keeps NaN
-  for (int64_t i = i0 + lane; i < i1; i += 32)
-    m = max(m, __float_as_int(to_f(state[b * ld + i])) & 0x7fffffff);
-  m = __reduce_max_sync(0xffffffffu, m);
-  const int e = scale_byte<INT8>(__int_as_float(m));
-  for (int64_t i = i0 + lane; i < i1; i += 32)
-    codes[s * n + i] = e == 255 ? 0 : encode<INT8>(to_f(state[b * ld + i]) * inverse_of(e));
-  if (lane == 0) scales[s * nb + k] = (uint8_t)e;
+  const int64_t c0 = ((int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kU;
+  uint4 raw[kU];
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {  // under way before the slots are looked at
+    const int64_t i = (c0 + u) * (32 * V) + lane * V;
+    raw[u] = i < n ? __ldcs(reinterpret_cast<const uint4 *>(state + b * ld + i))
+                   : make_uint4(0, 0, 0, 0);
+  }
+  const int64_t s = slot_of(slots, b, nslots);
+  if (s < 0 || named_later(slots, b, batch, s)) return;
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const int64_t i = (c0 + u) * (32 * V) + lane * V;
+    float v[V];
+    Vec<T>::get(raw[u], v);
+    int m = 0;  // the largest magnitude as bits: an order that keeps NaN
+#pragma unroll
+    for (int k = 0; k < V; ++k) m = max(m, __float_as_int(v[k]) & 0x7fffffff);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int e = scale_byte<INT8>(__int_as_float(m));
+    const float inv = inverse_of(min(e, 249));
+    if (i >= n) continue;
+    uint32_t q[V / 4];
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) q[k] = e == 255 ? 0u : encode4<INT8>(v + 4 * k, inv);
+    if (V == 4) *reinterpret_cast<uint32_t *>(codes + s * n + i) = q[0];
+    else *reinterpret_cast<uint2 *>(codes + s * n + i) = make_uint2(q[0], q[V / 4 - 1]);
+    if (lane % LANES == 0) scales[s * nb + i / (LANES * V)] = (uint8_t)e;
+  }
 }
 
 template <typename T, bool INT8>
-__global__ void load_kernel(T *state, int64_t ld, int64_t n, int block, int64_t nb,
-                            const int32_t *slots, int64_t nslots, const uint8_t *codes,
-                            const uint8_t *scales) {
+__global__ void __launch_bounds__(kThreads)
+    load_vec_kernel(T *__restrict__ state, int64_t ld, int64_t n, int shift, int64_t nb,
+                    const int32_t *__restrict__ slots, int64_t nslots,
+                    const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales) {
+  constexpr int V = Vec<T>::V;
   const int64_t b = blockIdx.y;
   const int64_t s = slot_of(slots, b, nslots);
   if (s < 0) return;
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= n) return;
-  const int e = scales[s * nb + i / block];
-  const float v = e == 255 ? __int_as_float(0x7fffffff) : decode<INT8>(codes[s * n + i]) * pow2_of(e);
-  state[b * ld + i] = from_f<T>(v);
+  const int64_t c0 = ((int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * kU;
+  const int lane = threadIdx.x & 31;
+  uint32_t q[kU][V / 4];
+  int e[kU];
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const int64_t i = (c0 + u) * (32 * V) + lane * V;
+    if (i < n) {
+      if (V == 4) {
+        q[u][0] = *reinterpret_cast<const uint32_t *>(codes + s * n + i);
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(codes + s * n + i);
+        q[u][0] = w.x;
+        q[u][V / 4 - 1] = w.y;
+      }
+      e[u] = scales[s * nb + (i >> shift)];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const int64_t i = (c0 + u) * (32 * V) + lane * V;
+    if (i >= n) continue;
+    float v[V];
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) decode4<INT8>(q[u][k], scale_of(e[u]), v + 4 * k);
+    __stcs(reinterpret_cast<uint4 *>(state + b * ld + i), Vec<T>::put(v));
+  }
 }
 
+// Rows anywhere: a lane takes single values, 32 apart, so that a warp's loads and
+// stores are of neighbouring ones; a warp has kPer * 32 values (whole blocks) under
+// way.
+constexpr int kPer = 8;
+
+template <typename T, bool INT8, int PER>  // PER: a block's values in a lane
+__global__ void __launch_bounds__(kThreads)
+    store_any_kernel(const T *__restrict__ state, int64_t ld, int64_t n, int64_t nb,
+                     const int32_t *__restrict__ slots, int64_t batch, int64_t nslots,
+                     uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+  const int64_t b = blockIdx.y;
+  const int lane = threadIdx.x & 31;
+  const int64_t i0 =
+      ((int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * (32 * kPer) + lane;
+  const int left = (int)max((int64_t)0, min(n - i0, (int64_t)32 * kPer));  // values from i0 on
+  const T *in = state + b * ld + i0;
+  float v[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) v[u] = 32 * u < left ? to_f(in[32 * u]) : 0.0f;
+  const int64_t s = slot_of(slots, b, nslots);
+  if (s < 0 || named_later(slots, b, batch, s)) return;
+  uint8_t *out = codes + s * n + i0;
+  uint8_t *sc = scales + s * nb + i0 / (32 * PER);
+#pragma unroll
+  for (int k = 0; k < kPer; k += PER) {
+    int m = 0;
+#pragma unroll
+    for (int u = k; u < k + PER; ++u) m = max(m, __float_as_int(v[u]) & 0x7fffffff);
+    const int e = scale_byte<INT8>(__int_as_float(__reduce_max_sync(0xffffffffu, m)));
+    const float inv = inverse_of(min(e, 249));
+#pragma unroll
+    for (int u = k; u < k + PER; ++u)
+      if (32 * u < left) out[32 * u] = e == 255 ? 0 : (uint8_t)encode1<INT8>(v[u], inv);
+    if (lane == 0 && 32 * k < left) sc[k / PER] = (uint8_t)e;
+  }
+}
+
+template <typename T, bool INT8>
+__global__ void __launch_bounds__(kThreads)
+    load_any_kernel(T *__restrict__ state, int64_t ld, int64_t n, int shift, int64_t nb,
+                    const int32_t *__restrict__ slots, int64_t nslots,
+                    const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales) {
+  const int64_t b = blockIdx.y;
+  const int64_t s = slot_of(slots, b, nslots);
+  if (s < 0) return;
+  const int64_t i0 = ((int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32) * (32 * kPer) +
+                     (threadIdx.x & 31);
+  const int left = (int)max((int64_t)0, min(n - i0, (int64_t)32 * kPer));
+  const uint8_t *in = codes + s * n + i0, *sc = scales + s * nb + (i0 >> shift);
+  const int k0 = (int)(i0 & ((1 << shift) - 1));  // i0's place in its block
+  T *out = state + b * ld + i0;
+  uint8_t q[kPer], e[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u)
+    if (32 * u < left) {
+      q[u] = in[32 * u];
+      e[u] = sc[(k0 + 32 * u) >> shift];
+    }
+#pragma unroll
+  for (int u = 0; u < kPer; ++u)
+    if (32 * u < left) out[32 * u] = from_f<T>(decode1<INT8>(q[u], scale_of(e[u])));
+}
+
+bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Whether every row of the state is on a 16-byte boundary and its codes can be
+// moved V at a time.
+template <typename T> bool on_boundaries(const StateCacheArgs &a) {
+  constexpr int V = Vec<T>::V;
+  return a.n % V == 0 && (a.batch == 1 || a.ld % V == 0) && aligned(a.state, 16) &&
+         aligned(a.codes, V);
+}
+int log2_of(int v) { return v == 32 ? 5 : v == 64 ? 6 : 7; }
+
 template <typename T, bool INT8> cudaError_t store(const StateCacheArgs &a) {
+  constexpr int V = Vec<T>::V;
   const int64_t nb = ceil_div(a.n, a.block);
-  store_kernel<T, INT8><<<dim3((unsigned)ceil_div(nb, 8), (unsigned)a.batch), 256, 0, a.stream>>>(
-      static_cast<const T *>(a.state), a.ld, a.n, a.block, nb, a.slots, a.batch, a.nslots,
-      static_cast<uint8_t *>(a.codes), a.scales);
+  const T *state = static_cast<const T *>(a.state);
+  uint8_t *codes = static_cast<uint8_t *>(a.codes);
+  if (on_boundaries<T>(a)) {
+    const dim3 grid((unsigned)ceil_div(a.n, (int64_t)kThreads * V * kU), (unsigned)a.batch);
+#define M2_STORE(block)                                                                      \
+  store_vec_kernel<T, INT8, block / V><<<grid, kThreads, 0, a.stream>>>(                     \
+      state, a.ld, a.n, nb, a.slots, a.batch, a.nslots, codes, a.scales)
+    if (a.block == 32) M2_STORE(32);
+    else if (a.block == 64) M2_STORE(64);
+    else M2_STORE(128);
+#undef M2_STORE
+  } else {
+    const dim3 grid((unsigned)ceil_div(a.n, kThreads * kPer), (unsigned)a.batch);
+#define M2_STORE(block)                                                                      \
+  store_any_kernel<T, INT8, block / 32><<<grid, kThreads, 0, a.stream>>>(                    \
+      state, a.ld, a.n, nb, a.slots, a.batch, a.nslots, codes, a.scales)
+    if (a.block == 32) M2_STORE(32);
+    else if (a.block == 64) M2_STORE(64);
+    else M2_STORE(128);
+#undef M2_STORE
+  }
   return cudaGetLastError();
 }
 template <typename T, bool INT8> cudaError_t load(const StateCacheArgs &a) {
+  constexpr int V = Vec<T>::V;
   const int64_t nb = ceil_div(a.n, a.block);
-  load_kernel<T, INT8><<<dim3((unsigned)ceil_div(a.n, 256), (unsigned)a.batch), 256, 0, a.stream>>>(
-      static_cast<T *>(a.state), a.ld, a.n, a.block, nb, a.slots, a.nslots,
-      static_cast<const uint8_t *>(a.codes), a.scales);
+  T *state = static_cast<T *>(a.state);
+  const uint8_t *codes = static_cast<const uint8_t *>(a.codes);
+  if (on_boundaries<T>(a))
+    load_vec_kernel<T, INT8>
+        <<<dim3((unsigned)ceil_div(a.n, (int64_t)kThreads * V * kU), (unsigned)a.batch), kThreads,
+           0, a.stream>>>(state, a.ld, a.n, log2_of(a.block), nb, a.slots, a.nslots, codes,
+                          a.scales);
+  else
+    load_any_kernel<T, INT8>
+        <<<dim3((unsigned)ceil_div(a.n, kThreads * kPer), (unsigned)a.batch), kThreads, 0,
+           a.stream>>>(state, a.ld, a.n, log2_of(a.block), nb, a.slots, a.nslots, codes, a.scales);
   return cudaGetLastError();
 }
 
