@@ -169,7 +169,8 @@ MAMBA2_API int mamba2_debug_stall_waits(int enable) {
   if (enable != 0 && enable != 1) return MAMBA2_ERR_INVALID_ARG;
   if (cudaDeviceSynchronize() != cudaSuccess) return MAMBA2_ERR_CUDA;
   if (set_step_stall((unsigned)enable) != cudaSuccess ||
-      set_prefill_tc_stall((unsigned)enable) != cudaSuccess)
+      set_prefill_tc_stall((unsigned)enable) != cudaSuccess ||
+      set_gated_scan_stall((unsigned)enable) != cudaSuccess)
     return MAMBA2_ERR_CUDA;
   return MAMBA2_OK;
 }
@@ -678,9 +679,10 @@ int gated_scan_dims_status(const mamba2_gated_scan_dims *d) {
   if (d->io_dtype != MAMBA2_F32 && d->io_dtype != MAMBA2_BF16) return MAMBA2_ERR_INVALID_ARG;
   if (!(d->decay_scale > 0.0f) || !std::isfinite(d->decay_scale)) return MAMBA2_ERR_INVALID_ARG;
   if (d->width % 8 != 0 || d->width > (1 << 20)) return MAMBA2_ERR_UNSUPPORTED;
-  // tokens and chunks are counted in 32 bits
-  if (d->batch >= (int64_t)1 << 31 || d->seqlen >= (int64_t)1 << 31 ||
-      d->batch * ceil_div(std::max<int64_t>(d->seqlen, 1), kGsChunk) >= (int64_t)1 << 31)
+  // tokens, sequences (in packed rows beside two bits) and tiles are counted in 32 bits
+  if (d->batch >= (int64_t)1 << 29 || d->seqlen >= (int64_t)1 << 31 ||
+      d->batch * ceil_div(std::max<int64_t>(d->seqlen, 1), kGsChunk) >=
+          ((int64_t)1 << 30) / ceil_div(d->width, gs_tile_width(d->io_dtype)))
     return MAMBA2_ERR_UNSUPPORTED;
   return MAMBA2_OK;
 }
@@ -727,14 +729,14 @@ MAMBA2_API size_t mamba2_gated_scan_workspace_size(const mamba2_gated_scan_dims 
                                                    int packed) {
   if (gated_scan_dims_status(dims) != MAMBA2_OK) return 0;
   return gated_scan_workspace(gated_scan_rows(dims, packed != 0), dims->seqlen, dims->width,
-                              dims->batch, packed != 0);
+                              dims->io_dtype, packed != 0);
 }
 
 MAMBA2_API size_t mamba2_gated_scan_backward_workspace_size(const mamba2_gated_scan_dims *dims,
                                                             int packed) {
   if (gated_scan_dims_status(dims) != MAMBA2_OK) return 0;
   return gated_scan_backward_workspace(gated_scan_rows(dims, packed != 0), dims->seqlen,
-                                       dims->width, dims->batch, packed != 0);
+                                       dims->width, dims->io_dtype, packed != 0);
 }
 
 MAMBA2_API size_t mamba2_gated_scan_checkpoint_count(const mamba2_gated_scan_dims *dims,

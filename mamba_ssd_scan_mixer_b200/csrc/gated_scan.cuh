@@ -6,6 +6,10 @@
 //     h_t = a h_{t-1} + m G x_t         y_t = h_t  [ * silu(z_t) ]
 #pragma once
 
+#include <cuda.h>
+
+#include <atomic>
+
 #include "common.cuh"
 
 namespace m2 {
@@ -43,14 +47,18 @@ struct GatedScanBackwardArgs {
 };
 
 cudaError_t gated_scan_prefill(const GatedScanArgs &a);
-size_t gated_scan_workspace(int64_t rows, int64_t L, int D, int64_t batch, bool packed);
+size_t gated_scan_workspace(int64_t rows, int64_t L, int D, int io, bool packed);
 cudaError_t gated_scan_step(const GatedScanArgs &a);
 cudaError_t gated_scan_backward(const GatedScanBackwardArgs &a);
-size_t gated_scan_backward_workspace(int64_t rows, int64_t L, int D, int64_t batch, bool packed);
+size_t gated_scan_backward_workspace(int64_t rows, int64_t L, int D, int io, bool packed);
+cudaError_t take_gated_scan_errors(unsigned int *out);
+cudaError_t set_gated_scan_stall(unsigned int v);
 // Sets *bad to whether the offsets of packed rows are wrong (and raises the flag).
 void gated_scan_check(const int32_t *cu, int64_t batch, int64_t L, unsigned int *bad,
                       cudaStream_t stream);
-cudaError_t take_gated_scan_errors(unsigned int *out);
+
+// Channels of a tile: one 128-byte row of the inputs.
+constexpr int gs_tile_width(int io) { return io == MAMBA2_BF16 ? 64 : 32; }
 
 // ---------------------------------------------------------------- arithmetic
 __device__ __forceinline__ float gs_sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
@@ -68,6 +76,145 @@ __device__ __forceinline__ Gate gs_gate(float r, float g, float ncs) {
   q.a = expf(q.la);
   q.m = sqrtf(-expm1f(2.0f * q.la));
   return q;
+}
+
+// Pairs of fp32 values in one 64-bit register: two multiply-adds an instruction.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ float2 unpack(F2 p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float sqrt_ap(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// sigmoid: the exponential overflows to infinity for very negative arguments, and its
+// reciprocal is then zero; NaN stays NaN.
+__device__ __forceinline__ F2 sigmoid2(F2 x) {
+  const float2 t = unpack(mul2(x, f2(-kLog2e)));
+  const float2 q = unpack(add2(f2(ex2(t.x), ex2(t.y)), f2(1.0f)));
+  return f2(rcp(q.x), rcp(q.y));
+}
+
+// a = 2^t and v = 1 - a^2 for t <= 0, both to a few half-steps relative to themselves:
+// t = k + f, |f| <= 1/2, 2^f - 1 = f P(f) (P: degree 5, fitted to 1.1e-8 of its value),
+// so that a - 1 = 2^k f P + (2^k - 1) cancels nowhere, and v = (1 - a)(1 + a).
+__device__ __forceinline__ void decay2(F2 t, F2 *a, F2 *v) {
+  const float2 u = unpack(t);
+  t = f2(max_nan(u.x, -125.0f), max_nan(u.y, -125.0f));  // 2^-125 is as good as zero
+  const F2 kk = add2(t, f2(12582912.0f));  // 1.5 2^23: rounds, and leaves k in the low bits
+  const F2 f = add2(t, mul2(add2(kk, f2(-12582912.0f)), f2(-1.0f)));
+  F2 q = fma2(f, f2(1.5403507859446108e-4f), f2(1.3390735257416964e-3f));
+  q = fma2(f, q, f2(9.618237614631653e-3f));
+  q = fma2(f, q, f2(5.550357326865196e-2f));
+  q = fma2(f, q, f2(2.4022649228572845e-1f));
+  q = mul2(f, fma2(f, q, f2(6.931471824645996e-1f)));
+  const float2 ki = unpack(kk);
+  const F2 s = f2(__int_as_float((__float_as_int(ki.x) << 23) + 0x3f800000),
+                  __int_as_float((__float_as_int(ki.y) << 23) + 0x3f800000));
+  const F2 less = fma2(s, q, add2(s, f2(-1.0f)));  // a - 1
+  *a = fma2(s, q, s);
+  *v = mul2(less, fma2(*a, f2(-1.0f), f2(-1.0f)));
+}
+
+// Tensor maps and the copies they describe.
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1,
+                                            int c2, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+// Host: whether something that belongs to a context (a launch attribute) has been set in
+// the current one.  Setting it twice is harmless, so that two threads may both do it.
+struct ContextOnce {
+  std::atomic<unsigned long long> seen[64] = {};
+  bool done() {
+    int d = 0;
+    if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 64) return false;
+    const unsigned long long id = current_context_id();
+    return id != 0 && seen[d].load(std::memory_order_acquire) == id;
+  }
+  void set() {
+    int d = 0;
+    if (cudaGetDevice(&d) == cudaSuccess && d >= 0 && d < 64)
+      seen[d].store(current_context_id(), std::memory_order_release);
+  }
+};
+
+// [rows][L][D] with a token stride of ld elements, in boxes of one tile; false if it
+// cannot be described.
+bool gs_tensor_map(CUtensorMap *m, int io, const void *base, int64_t rows, int64_t L, int D,
+                   int64_t ld);
+
+// Release / acquire of a flag at the GPU's scope.
+__device__ __forceinline__ void flag_set(unsigned int *p) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(1u) : "memory");
+}
+__device__ __forceinline__ unsigned int flag_get(const unsigned int *p) {
+  unsigned int v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// The map of a state across a stretch of tokens, h_out = A h_in + H, for two channels:
+// (A, A', H, H').  A sequence that begins inside the stretch leaves A = -0: what comes
+// in is then not multiplied by zero but left out, so that a NaN of the sequence before
+// stays there.  (A product of decays is never negative.)
+__device__ __forceinline__ float2 gs_through(float4 m, float2 h) {
+  h.x = __float_as_int(m.x) == (int)0x80000000 ? m.z : fmaf(m.x, h.x, m.z);
+  h.y = __float_as_int(m.y) == (int)0x80000000 ? m.w : fmaf(m.y, h.y, m.w);
+  return h;
+}
+// First one stretch, then another.
+__device__ __forceinline__ float4 gs_then(float4 one, float4 two) {
+  const float2 h = gs_through(two, make_float2(one.z, one.w));
+  return make_float4(__float_as_int(two.x) == (int)0x80000000 ? two.x : one.x * two.x,
+                     __float_as_int(two.y) == (int)0x80000000 ? two.y : one.y * two.y, h.x, h.y);
 }
 
 // Two neighbouring channels.
