@@ -681,8 +681,7 @@ int gated_scan_dims_status(const mamba2_gated_scan_dims *d) {
   if (d->width % 8 != 0 || d->width > (1 << 20)) return MAMBA2_ERR_UNSUPPORTED;
   // tokens, sequences (in packed rows beside two bits) and tiles are counted in 32 bits
   if (d->batch >= (int64_t)1 << 29 || d->seqlen >= (int64_t)1 << 31 ||
-      d->batch * ceil_div(std::max<int64_t>(d->seqlen, 1), kGsChunk) >=
-          ((int64_t)1 << 30) / ceil_div(d->width, gs_tile_width(d->io_dtype)))
+      gs_tiles(d->batch, std::max<int64_t>(d->seqlen, 1), d->width) >= (int64_t)1 << 30)
     return MAMBA2_ERR_UNSUPPORTED;
   return MAMBA2_OK;
 }
@@ -729,14 +728,14 @@ MAMBA2_API size_t mamba2_gated_scan_workspace_size(const mamba2_gated_scan_dims 
                                                    int packed) {
   if (gated_scan_dims_status(dims) != MAMBA2_OK) return 0;
   return gated_scan_workspace(gated_scan_rows(dims, packed != 0), dims->seqlen, dims->width,
-                              dims->io_dtype, packed != 0);
+                              packed != 0);
 }
 
 MAMBA2_API size_t mamba2_gated_scan_backward_workspace_size(const mamba2_gated_scan_dims *dims,
                                                             int packed) {
   if (gated_scan_dims_status(dims) != MAMBA2_OK) return 0;
   return gated_scan_backward_workspace(gated_scan_rows(dims, packed != 0), dims->seqlen,
-                                       dims->width, dims->io_dtype, packed != 0);
+                                       dims->width, packed != 0);
 }
 
 MAMBA2_API size_t mamba2_gated_scan_checkpoint_count(const mamba2_gated_scan_dims *dims,

@@ -1,18 +1,21 @@
 // Prefill and decode step of the gated linear recurrence (gated_scan.cuh).
 //
-// Prefill reads every input once.  The tokens of a row are cut into chunks of 128
-// and the channels into tiles of one 128-byte row; a tile is one chunk of one tile
-// of channels.  Resident blocks take tiles in order, chunk by chunk, from a counter:
+// Prefill reads every input once.  A tile is 64 tokens of 64 channels of a row;
+// resident blocks take tiles in order, all channels of a stretch of tokens before the
+// next stretch, from a counter:
 //   1. the tile's x, r and g arrive by TMA, two tiles ahead of the arithmetic;
-//   2. each thread turns the 16 (fp32: 8) tokens of its two channels into
-//      h_t = a_t h_{t-1} + b_t, keeps a and b in registers, and composes them; the
-//      segments' maps are composed through shared memory to the tile's (A, H);
-//   3. one warp publishes the tile's map and folds those of the chunks before it
-//      onto the state that the chunk group before left: the state entering the tile;
+//   2. each thread of the eight computing warps turns the 8 tokens of its two channels
+//      into h_t = a_t h_{t-1} + b_t, keeps a and b in registers, and composes them
+//      into the map of its segment, (A, H), in shared memory;
+//   3. meanwhile a ninth warp looks up the state entering the tile: it folds the
+//      maps of the tiles before it onto the state that the group of tiles before left.
+//      When the segments are there it publishes the tile's own map and fetches the
+//      tile after next;
 //   4. each thread runs its tokens from that state and writes y.
-// Every state is put together in an order fixed by the chunks' numbers alone, so that
-// results do not depend on timing.  A block waits only for tiles of lower numbers,
-// whose blocks are running: the tiles are handed out in order.
+// Nothing makes the whole block wait: warps meet at mbarriers only.  Every state is put
+// together in an order fixed by the tiles' numbers alone, so that results do not depend
+// on timing.  A block waits only for tiles of lower numbers, whose blocks are running:
+// the tiles are handed out in order.
 #include <algorithm>
 
 #include "gated_scan.cuh"
@@ -24,14 +27,16 @@ static __device__ unsigned int g_gs_stall = 0;  // mamba2_debug_stall_waits
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kTile = 64;   // tokens of a tile
+constexpr int kWidth = 64;  // channels of a tile: two for each lane
+constexpr int kWarps = 8;   // that compute
+constexpr int kTokens = kTile / kWarps;  // of a thread
+constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kStages = 2;
-constexpr int kRowBytes = 128;  // of a tile's token
-constexpr int kTensorBytes = kGsChunk * kRowBytes;
-constexpr int kStageBytes = 3 * kTensorBytes;
-// Chunks whose maps are folded one by one before a state is published again: more
+static_assert(kGsChunk % kTile == 0, "checkpoints lie between tiles");
+// Tiles whose maps are folded one by one before a state is published again: more
 // make a tile read more maps, fewer lengthen the chain of states.
-constexpr int kGroup = 16;
+constexpr int kGroup = 8;
 
 // Bits of a token's mark in packed rows: (sequence << 2) | last << 1 | first.
 constexpr int kFirst = 1, kLast = 2;
@@ -40,48 +45,44 @@ struct Scan {
   const float *ncs;  // [D] -c softplus(lam) log2(e)
   const void *z;
   int64_t ld_z, L;
-  int D, nblk, nch, rows, tiles;
+  int D, nblk, steps, rows, tiles;  // steps: tiles along a row's tokens
   const int *marks;         // packed rows: [L], else null
   const unsigned int *bad;  // packed rows: wrong offsets
   void *y;                  // or null: only the states entering the chunks are wanted
   const float *h_in;        // or null
   float *h_out, *ck;        // or null
-  float4 *maps;             // [tiles][kLanes]
-  float2 *states;           // [groups][rows][nblk][kLanes]
-  unsigned int *flags, *ticket;
-};
-
-template <typename T> struct Layout {
-  static constexpr int kWidth = kRowBytes / (int)sizeof(T);  // channels
-  static constexpr int kLanes = kWidth / 2;                  // threads a token
-  static constexpr int kSegs = kThreads / kLanes;
-  static constexpr int kTokens = kGsChunk / kSegs;  // of a thread
+  float4 *maps;             // [tiles][32]
+  float2 *states;           // [groups][rows][nblk][32]
+  unsigned int *ticket;
 };
 
 struct Tile {
-  int cb, row, chunk, left;
+  int cb, row, step, left;
 };
 
 template <typename T> struct Shared {
-  alignas(128) unsigned char in[kStages][kStageBytes];
-  alignas(16) int marks[kStages][kGsChunk];
-  float4 seg[Layout<T>::kSegs][Layout<T>::kLanes];
-  float2 enter[Layout<T>::kLanes];
-  uint64_t full[kStages];
+  static constexpr int kRow = kWidth * (int)sizeof(T);  // bytes of a token
+  static constexpr int kTensor = kTile * kRow;
+  alignas(128) unsigned char in[kStages][3 * kTensor];
+  alignas(16) int marks[kStages][kTile];
+  float4 seg[2][kWarps][32];
+  float2 enter[2][32];
+  uint64_t full[kStages], segs[2], entered[2];
   Tile tile[kStages];
 };
 
-// The counters reset, the decays' factor per channel, and for packed rows the
+// The counter and the records reset, the decays' factor per channel, and for packed rows the
 // offsets checked, the tokens marked and the states of empty sequences written.
-__global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, unsigned int *flags,
-                               int tiles, unsigned int *ticket, const int32_t *cu, int64_t batch,
+__global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, uint4 *records,
+                               int64_t nrecords, unsigned int *ticket, const int32_t *cu, int64_t batch,
                                int64_t L, int *marks, unsigned int *bad, float *h_out,
                                int states_in) {
   launch_dependents();
   const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t all = (int64_t)gridDim.x * blockDim.x;
   for (int64_t i = at; i < D; i += all) ncs[i] = -c * softplus_f(lam[i]) * kLog2e;
-  for (int64_t i = at; i < tiles; i += all) flags[i] = 0;
+  for (int64_t i = at; i < nrecords; i += all)
+    records[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
   if (at == 0) *ticket = 0;
   if (cu == nullptr) return;
   // every block looks at all offsets, so that none acts on wrong ones
@@ -109,32 +110,22 @@ __global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, uns
         for (int d = threadIdx.x % 32; d < D; d += 32) h_out[s * D + d] = 0.0f;
 }
 
-template <typename T> __device__ __forceinline__ F2 row_pair(const unsigned char *p);
-template <> __device__ __forceinline__ F2 row_pair<float>(const unsigned char *p) {
-  const float2 v = *reinterpret_cast<const float2 *>(p);
-  return f2(v.x, v.y);
-}
-template <> __device__ __forceinline__ F2 row_pair<__nv_bfloat16>(const unsigned char *p) {
-  const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
-  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-
-// Steps 2: a and b of the thread's tokens, and their composition.
-template <typename T, bool FULL, bool PACKED>
+// Step 2: a and b of the thread's tokens, and their composition.
+template <typename T, bool FULL, bool PACKED, bool NEAR>
 __device__ __forceinline__ float4 make_maps(const unsigned char *in, const int *marks, F2 ncs, int n,
-                                            const Scan &p, int d, F2 (&a)[Layout<T>::kTokens],
-                                            F2 (&b)[Layout<T>::kTokens]) {
+                                            const Scan &p, int d, F2 (&a)[kTokens],
+                                            F2 (&b)[kTokens]) {
+  constexpr int kRow = Shared<T>::kRow, kTensor = Shared<T>::kTensor;
   F2 A = f2(1.0f), H = f2(0.0f);
   float4 map = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < Layout<T>::kTokens; ++i) {
-    const unsigned char *row = in + i * kRowBytes;
-    const F2 x = row_pair<T>(row), R = sigmoid2(row_pair<T>(row + kTensorBytes)),
-             G = sigmoid2(row_pair<T>(row + 2 * kTensorBytes));
-    F2 v;
-    decay2(mul2(ncs, R), &a[i], &v);
-    const float2 vv = unpack(v);
-    b[i] = mul2(mul2(f2(sqrt_ap(vv.x), sqrt_ap(vv.y)), G), x);
+  for (int i = 0; i < kTokens; ++i) {
+    const unsigned char *row = in + i * kRow;
+    const Coeffs c =
+        coefficients<NEAR>(gs_pair<T>(row), gs_clamped<T>(row + kTensor),
+                           gs_clamped<T>(row + 2 * kTensor), ncs);
+    a[i] = c.a;
+    b[i] = c.b;
     if (!FULL && i >= n) {
       a[i] = f2(1.0f);
       b[i] = f2(0.0f);
@@ -142,7 +133,8 @@ __device__ __forceinline__ float4 make_maps(const unsigned char *in, const int *
     if (PACKED) {
       if ((FULL || i < n) && (marks[i] & kFirst)) {
         if (p.h_in != nullptr && d < p.D) {
-          const float2 h = *reinterpret_cast<const float2 *>(p.h_in + (int64_t)(marks[i] >> 2) * p.D + d);
+          const float2 h =
+              *reinterpret_cast<const float2 *>(p.h_in + (int64_t)(marks[i] >> 2) * p.D + d);
           b[i] = fma2(a[i], f2(h.x, h.y), b[i]);
         }
         a[i] = f2(-0.0f);
@@ -166,88 +158,186 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float2 v) {
   *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
 }
 
-template <typename T, bool PACKED, bool GATED>
-__global__ void __launch_bounds__(kThreads, 2)
-    gs_prefill_kernel(const __grid_constant__ CUtensorMap map_x,
-                      const __grid_constant__ CUtensorMap map_r,
-                      const __grid_constant__ CUtensorMap map_g, const Scan p) {
-  using Lay = Layout<T>;
-  constexpr int kLanes = Lay::kLanes, kTokens = Lay::kTokens;
-  extern __shared__ __align__(128) unsigned char raw[];
-  Shared<T> &sm = *reinterpret_cast<Shared<T> *>(raw);
-  const int tid = threadIdx.x, lane = tid % kLanes, seg = tid / kLanes;
-  if (test_stall(&g_gs_stall, &g_gs_errors)) return;
-  if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[s], 1);
-    fence_mbar_init();
-  }
-  __syncthreads();
-  grid_dependency_wait();
-  if (PACKED && *p.bad) return;
-
-  // one thread: tile t's copies, into stage s
+// Step 3: the ninth warp.
+template <typename T, bool PACKED>
+__device__ __forceinline__ void look_up(Shared<T> &sm, const CUtensorMap &map_x,
+                                        const CUtensorMap &map_r, const CUtensorMap &map_g,
+                                        const Scan &p) {
+  const int lane = threadIdx.x & 31;
+  const int per_step = p.rows * p.nblk;
+  // one lane: tile t's copies, into stage s
   auto fetch = [&](int s, int t) {
     Tile q;
     q.left = p.tiles - t;
     q.cb = t % p.nblk;
     q.row = t / p.nblk % p.rows;
-    q.chunk = t / p.nblk / p.rows;
+    q.step = t / per_step;
     sm.tile[s] = q;
     if (q.left <= 0) {
       mbar_arrive(&sm.full[s]);
       return;
     }
-    const int t0 = q.chunk * kGsChunk, n = (int)min((int64_t)kGsChunk, p.L - t0);
+    const int t0 = q.step * kTile, n = (int)min((int64_t)kTile, p.L - t0);
     // (whole 16-byte groups of marks; the array is padded)
     const uint32_t mark_bytes = PACKED ? (n * 4 + 15) / 16 * 16 : 0;
-    mbar_arrive_expect_tx(&sm.full[s], kStageBytes + mark_bytes);
+    mbar_arrive_expect_tx(&sm.full[s], 3 * Shared<T>::kTensor + mark_bytes);
     unsigned char *in = sm.in[s];
-    tma_load_3d(in, &map_x, q.cb * Lay::kWidth, t0, q.row, &sm.full[s]);
-    tma_load_3d(in + kTensorBytes, &map_r, q.cb * Lay::kWidth, t0, q.row, &sm.full[s]);
-    tma_load_3d(in + 2 * kTensorBytes, &map_g, q.cb * Lay::kWidth, t0, q.row, &sm.full[s]);
+    tma_load_3d(in, &map_x, q.cb * kWidth, t0, q.row, &sm.full[s]);
+    tma_load_3d(in + Shared<T>::kTensor, &map_r, q.cb * kWidth, t0, q.row, &sm.full[s]);
+    tma_load_3d(in + 2 * Shared<T>::kTensor, &map_g, q.cb * kWidth, t0, q.row, &sm.full[s]);
     if (PACKED) bulk_g2s(sm.marks[s], p.marks + t0, mark_bytes, &sm.full[s]);
   };
-  constexpr int kFetcher = 32;
-  if (tid == kFetcher)
+  if (lane == 0)
     for (int s = 0; s < kStages; ++s) fetch(s, (int)atomicAdd(p.ticket, 1u));
+  __syncwarp();
 
   for (int it = 0;; ++it) {
-    const int s = it % kStages;
-    const bool arrived = mbar_wait_bounded(&sm.full[s], (it / kStages) & 1, &g_gs_errors);
-    // (also: the last tile's segments have been read)
-    if (!__syncthreads_and(arrived)) {
-      // a wait ran out: what this block has under way lands before it leaves
-      if (tid == kFetcher)
-        for (int i = it; i < it + kStages; ++i)
-          mbar_wait_bounded(&sm.full[i % kStages], (i / kStages) & 1, &g_gs_errors);
-      return;
-    }
+    const int s = it % kStages, half = it & 1;
+    const uint32_t phase = (it >> 1) & 1;
     const Tile q = sm.tile[s];
     if (q.left <= 0) return;  // so is every later tile's: no copy is under way
     int next = 0;
-    if (tid == kFetcher) next = (int)atomicAdd(p.ticket, 1u);  // wanted after step 2
-    const int t0 = q.chunk * kGsChunk, n = (int)min((int64_t)kGsChunk, p.L - t0);
-    const int d = q.cb * Lay::kWidth + 2 * lane, first = seg * kTokens;
+    if (lane == 0) next = (int)atomicAdd(p.ticket, 1u);  // wanted when the segments are there
+    const int d = q.cb * kWidth + 2 * lane, mine = q.row * p.nblk + q.cb;
+    const int tile = q.step * per_step + mine;
+    const int group = q.step / kGroup, in_group = q.step % kGroup;
+    const bool last = q.step == p.steps - 1;
+    bool published = false, entered = false, based = group == 0;
+    int folded = 0;  // maps of the group's tiles before this one, and their base
+    const float2 *base = p.states + ((int64_t)(group - 1) * per_step + mine) * 32 + lane;
+    const float4 *before = p.maps + ((int64_t)group * kGroup * per_step + mine) * 32 + lane;
+    float2 h = make_float2(0.0f, 0.0f);
+    if (!PACKED && q.step == 0 && p.h_in != nullptr && d < p.D)
+      h = *reinterpret_cast<const float2 *>(p.h_in + (int64_t)q.row * p.D + d);
+    float4 map;
+    unsigned long long since = 0;
+    for (;;) {
+      if (!published &&
+          __all_sync(0xffffffffu, entered ? mbar_try_wait(&sm.segs[half], phase)
+                                          : mbar_test(&sm.segs[half], phase))) {
+        map = sm.seg[half][0][lane];
+#pragma unroll
+        for (int k = 1; k < kWarps; ++k) map = gs_then(map, sm.seg[half][k][lane]);
+        if (q.step == 0) {  // known whole: nothing before it counts
+          const float2 e = gs_through(map, h);
+          map = make_float4(-0.0f, -0.0f, e.x, e.y);
+        }
+        if (!last && in_group != kGroup - 1) record_put(p.maps + (int64_t)tile * 32 + lane, map);
+        if (lane == 0) fetch(s, next);
+        __syncwarp();
+        published = true;
+      }
+      if (!entered) {
+        float2 b = make_float2(0.0f, 0.0f);
+        float4 m[kGroup - 1];
+        if (!based) b = record_get(base);
+        unsigned int there = 0;
+#pragma unroll
+        for (int k = 0; k < kGroup - 1; ++k)
+          if (k >= folded && k < in_group) m[k] = record_get(before + (int64_t)k * per_step * 32);
+#pragma unroll
+        for (int k = 0; k < kGroup - 1; ++k)
+          if (k < folded || k >= in_group || is_set(m[k])) there |= 1u << k;
+        if (based || is_set(b)) there |= 1u << 31;
+        there = __reduce_and_sync(0xffffffffu, there);
+        if (there >> 31) {
+          if (!based) h = b;
+          based = true;
+#pragma unroll
+          for (int k = 0; k < kGroup - 1; ++k)
+            if (k == folded && k < in_group && (there >> k & 1)) {
+              h = gs_through(m[k], h);
+              ++folded;
+            }
+          entered = folded == in_group;
+        }
+        if (entered) {
+          sm.enter[half][lane] = h;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.entered[half]);
+          if (p.ck != nullptr && q.step % (kGsChunk / kTile) == 0 && d < p.D) {
+            const int64_t nch = (p.L + kGsChunk - 1) / kGsChunk;
+            *reinterpret_cast<float2 *>(
+                p.ck + ((int64_t)q.row * nch + q.step / (kGsChunk / kTile)) * p.D + d) = h;
+          }
+        }
+      }
+      if (published && entered) break;
+      const unsigned long long now = globaltimer_ns();
+      if (since == 0) since = now;
+      if (__any_sync(0xffffffffu, now - since > kWaitLimitNs)) {
+        // what this block has under way lands before the warp leaves
+        if (lane == 0) {
+          atomicOr(&g_gs_errors, kErrWaitTimeout);
+          for (int i = it + published; i < it + published + kStages; ++i)
+            mbar_wait_bounded(&sm.full[i % kStages], (i / kStages) & 1, &g_gs_errors);
+        }
+        return;
+      }
+    }
+    if (!last && in_group == kGroup - 1)
+      record_put(p.states + ((int64_t)group * per_step + mine) * 32 + lane, gs_through(map, h));
+  }
+}
+
+template <typename T, bool PACKED, bool GATED>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+    gs_prefill_kernel(const __grid_constant__ CUtensorMap map_x,
+                      const __grid_constant__ CUtensorMap map_r,
+                      const __grid_constant__ CUtensorMap map_g, const Scan p) {
+  extern __shared__ __align__(128) unsigned char raw[];
+  Shared<T> &sm = *reinterpret_cast<Shared<T> *>(raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (test_stall(&g_gs_stall, &g_gs_errors)) return;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[s], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.segs[s], kWarps);
+      mbar_init(&sm.entered[s], 1);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  if (PACKED && *p.bad) return;
+  if (warp == kWarps) {
+    look_up<T, PACKED>(sm, map_x, map_r, map_g, p);
+    return;
+  }
+
+  const int first = warp * kTokens;
+  for (int it = 0;; ++it) {
+    const int s = it % kStages, half = it & 1;
+    const uint32_t phase = (it >> 1) & 1;
+    if (!mbar_wait_bounded(&sm.full[s], (it / kStages) & 1, &g_gs_errors)) return;
+    const Tile q = sm.tile[s];
+    if (q.left <= 0) return;
+    const int t0 = q.step * kTile, n = (int)min((int64_t)kTile, p.L - t0);
+    const int d = q.cb * kWidth + 2 * lane;
     const bool real = d < p.D;
     float2 ncs = make_float2(0.0f, 0.0f);
     if (real) ncs = *reinterpret_cast<const float2 *>(p.ncs + d);
     F2 a[kTokens], b[kTokens];
-    const unsigned char *in = sm.in[s] + first * kRowBytes + lane * (2 * (int)sizeof(T));
+    const unsigned char *in = sm.in[s] + first * Shared<T>::kRow + lane * (2 * (int)sizeof(T));
     const int *marks = sm.marks[s] + first;
-    sm.seg[seg][lane] =
-        n == kGsChunk
-            ? make_maps<T, true, PACKED>(in, marks, f2(ncs.x, ncs.y), n - first, p, d, a, b)
-            : make_maps<T, false, PACKED>(in, marks, f2(ncs.x, ncs.y), n - first, p, d, a, b);
+    const F2 k = f2(ncs.x, ncs.y);
+    float4 map;
+    if (__all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f))
+      map = n == kTile ? make_maps<T, true, PACKED, true>(in, marks, k, n - first, p, d, a, b)
+                       : make_maps<T, false, PACKED, true>(in, marks, k, n - first, p, d, a, b);
+    else
+      map = make_maps<T, false, PACKED, false>(in, marks, k, n - first, p, d, a, b);
+    sm.seg[half][warp][lane] = map;
     int ends = 0;  // packed rows: which of the thread's tokens end a sequence
     if (PACKED && p.h_out != nullptr) {
 #pragma unroll
       for (int i = 0; i < kTokens; ++i)
         if (i < n - first && (marks[i] & kLast)) ends |= 1 << i;
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.segs[half]);
     const int64_t token = (int64_t)q.row * p.L + t0 + first;
-    __syncthreads();
-    if (tid == kFetcher) fetch(s, next);
-    typename Pair<T>::V gate[GATED ? kTokens : 1];  // under way while the states are looked up
+    typename Pair<T>::V gate[GATED ? kTokens : 1];  // under way while the state is looked up
     if (GATED) {
       const T *z = static_cast<const T *>(p.z) + token * p.ld_z + d;
 #pragma unroll
@@ -257,75 +347,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           gate[i] = *reinterpret_cast<const typename Pair<T>::V *>(z + i * p.ld_z);
       }
     }
-
-    const bool last_chunk = q.chunk == p.nch - 1;
-    if (tid < 32) {
-      float4 map = sm.seg[0][lane];
-      for (int k = 1; k < Lay::kSegs; ++k) map = gs_then(map, sm.seg[k][lane]);
-      float2 h = make_float2(0.0f, 0.0f);
-      if (q.chunk == 0) {
-        if (!PACKED && p.h_in != nullptr && real)
-          h = *reinterpret_cast<const float2 *>(p.h_in + (int64_t)q.row * p.D + d);
-        const float2 e = gs_through(map, h);  // known whole: nothing before it counts
-        map = make_float4(-0.0f, -0.0f, e.x, e.y);
-      }
-      const int per_chunk = p.rows * p.nblk, mine = q.row * p.nblk + q.cb;
-      const int tile = q.chunk * per_chunk + mine;
-      const int group = q.chunk / kGroup, in_group = q.chunk % kGroup;
-      if (!last_chunk && in_group != kGroup - 1) {
-        if (tid < kLanes) __stcg(p.maps + (int64_t)tile * kLanes + lane, map);
-        __syncwarp();
-        if (tid == 0) flag_set(p.flags + tile);
-      }
-      if (q.chunk > 0) {
-        // the chunks of the group before this one, and the last of the group before
-        const int from = group > 0 ? group * kGroup - 1 : 0, need = q.chunk - from;
-        const unsigned int *flag = p.flags + (int64_t)(from + tid) * per_chunk + mine;
-        bool ready = tid >= need || flag_get(flag);
-        if (!__all_sync(0xffffffffu, ready)) {
-          const unsigned long long since = globaltimer_ns();
-          for (;;) {
-            ready = ready || flag_get(flag);
-            if (__all_sync(0xffffffffu, ready)) break;
-            const bool late = globaltimer_ns() - since > kWaitLimitNs;
-            if (__any_sync(0xffffffffu, late)) {
-              if (tid == 0) atomicOr(&g_gs_errors, kErrWaitTimeout);
-              break;
-            }
-          }
-        }
-        __syncwarp();
-        if (group > 0)
-          h = __ldcg(p.states + ((int64_t)(group - 1) * per_chunk + mine) * kLanes + lane);
-        for (int k0 = 0; k0 < in_group; k0 += 8) {
-          float4 m[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k0 + k < in_group)
-              m[k] = __ldcg(p.maps + ((int64_t)(group * kGroup + k0 + k) * per_chunk + mine) * kLanes + lane);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k0 + k < in_group) h = gs_through(m[k], h);
-        }
-        if (!last_chunk && in_group == kGroup - 1) {
-          if (tid < kLanes)
-            __stcg(p.states + ((int64_t)group * per_chunk + mine) * kLanes + lane,
-                   gs_through(map, h));
-          __syncwarp();
-          if (tid == 0) flag_set(p.flags + tile);
-        }
-      }
-      if (tid < kLanes) {
-        sm.enter[lane] = h;
-        if (p.ck != nullptr && real)
-          *reinterpret_cast<float2 *>(p.ck + ((int64_t)q.row * p.nch + q.chunk) * p.D + d) = h;
-      }
-    }
-    __syncthreads();
+    if (!mbar_wait_bounded(&sm.segs[half], phase, &g_gs_errors) ||
+        !mbar_wait_bounded(&sm.entered[half], phase, &g_gs_errors))
+      return;
     if (p.y == nullptr) continue;
 
-    float2 h = sm.enter[lane];
-    for (int k = 0; k < seg; ++k) h = gs_through(sm.seg[k][lane], h);
+    float2 h = sm.enter[half][lane];
+    for (int k = 0; k < warp; ++k) h = gs_through(sm.seg[half][k][lane], h);
     F2 hh = f2(h.x, h.y);
     T *y = static_cast<T *>(p.y) + token * p.D + d;
 #pragma unroll
@@ -349,7 +377,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                                       d) = unpack(hh);
       }
     }
-    if (!PACKED && p.h_out != nullptr && last_chunk && real && first < n && n <= first + kTokens)
+    if (!PACKED && p.h_out != nullptr && q.step == p.steps - 1 && real && first < n &&
+        n <= first + kTokens)
       // (tokens behind the last leave the state as it is)
       *reinterpret_cast<float2 *>(p.h_out + (int64_t)q.row * p.D + d) = unpack(hh);
   }
@@ -393,23 +422,20 @@ template <typename T> In<T> inputs(const GatedScanArgs &a) {
 
 // Where the parts of the workspace are.
 struct Plan {
-  int nblk, nch, lanes;
+  int nblk, steps;
   int64_t tiles, groups;
-  size_t ncs, flags, maps, states, marks, total;
+  size_t ncs, maps, states, marks, total;
 };
-Plan plan_of(int64_t rows, int64_t L, int D, int io, bool packed) {
+Plan plan_of(int64_t rows, int64_t L, int D, bool packed) {
   Plan p;
-  const int width = gs_tile_width(io);
-  p.lanes = width / 2;
-  p.nblk = (int)ceil_div(D, width);
-  p.nch = (int)ceil_div(L, kGsChunk);
-  p.tiles = rows * p.nch * p.nblk;
-  p.groups = p.nch / kGroup;
+  p.nblk = (int)ceil_div(D, kWidth);
+  p.steps = (int)ceil_div(L, kTile);
+  p.tiles = rows * p.steps * p.nblk;
+  p.groups = p.steps / kGroup;
   p.ncs = 256;  // after the counter and the flag of wrong offsets
-  p.flags = p.ncs + align_up((size_t)D * 4, 256);
-  p.maps = p.flags + align_up((size_t)p.tiles * 4, 256);
-  p.states = p.maps + (p.nch > 1 ? align_up((size_t)p.tiles * p.lanes * 16, 256) : 0);
-  p.marks = p.states + align_up((size_t)p.groups * rows * p.nblk * p.lanes * 8, 256);
+  p.maps = p.ncs + align_up((size_t)D * 4, 256);
+  p.states = p.maps + (p.steps > 1 ? (size_t)p.tiles * 32 * 16 : 0);
+  p.marks = p.states + (size_t)(p.groups * rows * p.nblk) * 32 * 8;
   p.total = p.marks + (packed ? align_up((size_t)L * 4, 256) : 0);
   return p;
 }
@@ -425,7 +451,8 @@ int sm_count() {
 template <typename T, bool PACKED, bool GATED>
 cudaError_t launch(const GatedScanArgs &a, const CUtensorMap (&m)[3], const Scan &p) {
   constexpr size_t smem = sizeof(Shared<T>);
-  static_assert(2 * (smem + 2048) <= 227 * 1024, "two blocks to an SM");
+  constexpr int kResident = sizeof(T) == 2 ? 3 : 2;
+  static_assert(kResident * (smem + 2048) <= 227 * 1024, "blocks to an SM");
   static ContextOnce once;
   if (!once.done()) {
     const cudaError_t e = cudaFuncSetAttribute(
@@ -434,7 +461,7 @@ cudaError_t launch(const GatedScanArgs &a, const CUtensorMap (&m)[3], const Scan
     once.set();
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min(p.tiles, 2 * sm_count()), 1, 1);
+  cfg.gridDim = dim3((unsigned)std::min(p.tiles, kResident * sm_count()), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = a.stream;
@@ -449,7 +476,7 @@ cudaError_t launch(const GatedScanArgs &a, const CUtensorMap (&m)[3], const Scan
 template <typename T> cudaError_t prefill(const GatedScanArgs &a) {
   const int64_t rows = a.rows();
   const bool packed = a.cu != nullptr;
-  const Plan w = plan_of(rows, a.L, a.D, a.io, packed);
+  const Plan w = plan_of(rows, a.L, a.D, packed);
   Scan p;
   p.ncs = reinterpret_cast<float *>(a.ws + w.ncs);
   p.z = a.z;
@@ -457,7 +484,7 @@ template <typename T> cudaError_t prefill(const GatedScanArgs &a) {
   p.L = a.L;
   p.D = a.D;
   p.nblk = w.nblk;
-  p.nch = w.nch;
+  p.steps = w.steps;
   p.rows = (int)rows;
   p.tiles = (int)w.tiles;
   p.marks = packed ? reinterpret_cast<int *>(a.ws + w.marks) : nullptr;
@@ -469,16 +496,17 @@ template <typename T> cudaError_t prefill(const GatedScanArgs &a) {
   p.ck = a.ck;
   p.maps = reinterpret_cast<float4 *>(a.ws + w.maps);
   p.states = reinterpret_cast<float2 *>(a.ws + w.states);
-  p.flags = reinterpret_cast<unsigned int *>(a.ws + w.flags);
   CUtensorMap m[3];
   if (!gs_tensor_map(&m[0], a.io, a.x, rows, a.L, a.D, a.ld_x) ||
       !gs_tensor_map(&m[1], a.io, a.r, rows, a.L, a.D, a.ld_r) ||
       !gs_tensor_map(&m[2], a.io, a.g, rows, a.L, a.D, a.ld_g))
     return cudaErrorInvalidValue;
-  const int64_t work = std::max(std::max<int64_t>(a.D, w.tiles), packed ? a.L : 0);
-  gs_prep_kernel<<<(unsigned)std::min<int64_t>(ceil_div(work, 256), 148), 256, 0, a.stream>>>(
-      a.lam, a.c, a.D, const_cast<float *>(p.ncs), p.flags, p.tiles, p.ticket, a.cu, a.batch, a.L,
-      const_cast<int *>(p.marks), const_cast<unsigned int *>(p.bad), p.h_out, a.states_in);
+  const int64_t nrecords = (int64_t)(w.marks - w.maps) / 16;  // maps and states, side by side
+  const int64_t work = std::max(std::max<int64_t>(a.D, nrecords), packed ? a.L : 0);
+  gs_prep_kernel<<<(unsigned)std::min<int64_t>(ceil_div(work, 256), 148 * 4), 256, 0, a.stream>>>(
+      a.lam, a.c, a.D, const_cast<float *>(p.ncs), reinterpret_cast<uint4 *>(a.ws + w.maps),
+      nrecords, p.ticket, a.cu, a.batch, a.L, const_cast<int *>(p.marks),
+      const_cast<unsigned int *>(p.bad), p.h_out, a.states_in);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const bool gated = a.z != nullptr && a.y != nullptr;
@@ -535,7 +563,7 @@ bool gs_tensor_map(CUtensorMap *m, int io, const void *base, int64_t rows, int64
   const uint64_t esz = bf ? 2 : 4;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)L, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {(uint64_t)ld * esz, (uint64_t)ld * esz * (uint64_t)L};
-  const cuuint32_t box[3] = {(cuuint32_t)gs_tile_width(io), (cuuint32_t)kGsChunk, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)kWidth, (cuuint32_t)kTile, 1};
   const cuuint32_t one[3] = {1, 1, 1};
   return encode(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
                 const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -543,8 +571,8 @@ bool gs_tensor_map(CUtensorMap *m, int io, const void *base, int64_t rows, int64
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t gated_scan_workspace(int64_t rows, int64_t L, int D, int io, bool packed) {
-  return plan_of(rows, L, D, io, packed).total;
+size_t gated_scan_workspace(int64_t rows, int64_t L, int D, bool packed) {
+  return plan_of(rows, L, D, packed).total;
 }
 
 cudaError_t gated_scan_prefill(const GatedScanArgs &a) {

@@ -47,18 +47,20 @@ struct GatedScanBackwardArgs {
 };
 
 cudaError_t gated_scan_prefill(const GatedScanArgs &a);
-size_t gated_scan_workspace(int64_t rows, int64_t L, int D, int io, bool packed);
+size_t gated_scan_workspace(int64_t rows, int64_t L, int D, bool packed);
 cudaError_t gated_scan_step(const GatedScanArgs &a);
 cudaError_t gated_scan_backward(const GatedScanBackwardArgs &a);
-size_t gated_scan_backward_workspace(int64_t rows, int64_t L, int D, int io, bool packed);
+size_t gated_scan_backward_workspace(int64_t rows, int64_t L, int D, bool packed);
 cudaError_t take_gated_scan_errors(unsigned int *out);
 cudaError_t set_gated_scan_stall(unsigned int v);
 // Sets *bad to whether the offsets of packed rows are wrong (and raises the flag).
 void gated_scan_check(const int32_t *cu, int64_t batch, int64_t L, unsigned int *bad,
                       cudaStream_t stream);
 
-// Channels of a tile: one 128-byte row of the inputs.
-constexpr int gs_tile_width(int io) { return io == MAMBA2_BF16 ? 64 : 32; }
+// Tiles of 64 tokens and 64 channels in a call: they are counted in 32 bits.
+inline int64_t gs_tiles(int64_t rows, int64_t L, int64_t D) {
+  return rows * ceil_div(L, 64) * ceil_div(D, 64);
+}
 
 // ---------------------------------------------------------------- arithmetic
 __device__ __forceinline__ float gs_sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
@@ -139,25 +141,88 @@ __device__ __forceinline__ F2 sigmoid2(F2 x) {
   return f2(rcp(q.x), rcp(q.y));
 }
 
-// a = 2^t and v = 1 - a^2 for t <= 0, both to a few half-steps relative to themselves:
-// t = k + f, |f| <= 1/2, 2^f - 1 = f P(f) (P: degree 5, fitted to 1.1e-8 of its value),
-// so that a - 1 = 2^k f P + (2^k - 1) cancels nowhere, and v = (1 - a)(1 + a).
-__device__ __forceinline__ void decay2(F2 t, F2 *a, F2 *v) {
-  const float2 u = unpack(t);
-  t = f2(max_nan(u.x, -125.0f), max_nan(u.y, -125.0f));  // 2^-125 is as good as zero
-  const F2 kk = add2(t, f2(12582912.0f));  // 1.5 2^23: rounds, and leaves k in the low bits
-  const F2 f = add2(t, mul2(add2(kk, f2(-12582912.0f)), f2(-1.0f)));
+// 2^f - 1 = f P(f) for |f| <= 1/2; P of degree 5, fitted here to 1.1e-8 of its value.
+__device__ __forceinline__ F2 exp2m1(F2 f) {
   F2 q = fma2(f, f2(1.5403507859446108e-4f), f2(1.3390735257416964e-3f));
   q = fma2(f, q, f2(9.618237614631653e-3f));
   q = fma2(f, q, f2(5.550357326865196e-2f));
   q = fma2(f, q, f2(2.4022649228572845e-1f));
-  q = mul2(f, fma2(f, q, f2(6.931471824645996e-1f)));
+  return mul2(f, fma2(f, q, f2(6.931471824645996e-1f)));
+}
+
+// a = 2^t and less = a - 1 for t <= 0, both to a few half-steps relative to themselves.
+// NEAR: t >= -1/2 for every channel of the warp (its lam's), so that a > 0.7; else
+// t = k + f and a - 1 = 2^k (2^f - 1) + (2^k - 1), which cancels nowhere.
+template <bool NEAR> __device__ __forceinline__ void decay2(F2 t, F2 *a, F2 *less) {
+  if (NEAR) {
+    *less = exp2m1(t);
+    *a = add2(*less, f2(1.0f));
+    return;
+  }
+  const float2 u = unpack(t);
+  t = f2(max_nan(u.x, -125.0f), max_nan(u.y, -125.0f));  // 2^-125 is as good as zero
+  const F2 kk = add2(t, f2(12582912.0f));  // 1.5 2^23: rounds, and leaves k in the low bits
+  const F2 q = exp2m1(fma2(add2(kk, f2(-12582912.0f)), f2(-1.0f), t));
   const float2 ki = unpack(kk);
   const F2 s = f2(__int_as_float((__float_as_int(ki.x) << 23) + 0x3f800000),
                   __int_as_float((__float_as_int(ki.y) << 23) + 0x3f800000));
-  const F2 less = fma2(s, q, add2(s, f2(-1.0f)));  // a - 1
+  *less = fma2(s, q, add2(s, f2(-1.0f)));
   *a = fma2(s, q, s);
-  *v = mul2(less, fma2(*a, f2(-1.0f), f2(-1.0f)));
+}
+
+// The recurrence's coefficients for two channels of a token: a and b = m G x.
+//
+// What bounds them is the unit of ex2, rcp and sqrt (16 lanes a clock and SM): R and G
+// share a reciprocal, R = (1 + e^-g) / P and G = (1 + e^-r) / P with P their
+// denominators' product.  r and g come cut off at -43 for that (gs_clamp), so that P
+// stays finite; a gate below 2^-62 counts as 2^-62.  m is taken of v = 1 - a^2 times
+// 2^-70, where the square root flushes v < 2^-56 to zero: r = -inf leaves the state
+// exactly as it was (for c softplus(lam) < 32), and an increment lost is below 4e-9 of
+// x.  The 2^35 that m then lacks is in G.
+struct Coeffs {
+  F2 a, b, t, less, R, G, m;  // (G and m scaled by 2^35 and 2^-35)
+};
+constexpr float kGateScale = 34359738368.0f;  // 2^35
+template <bool NEAR>
+__device__ __forceinline__ Coeffs coefficients(F2 x, F2 r, F2 g, F2 ncs) {
+  constexpr float down = 1.0f / kGateScale, down2 = down * down;
+  Coeffs c;
+  const float2 er = unpack(mul2(r, f2(-kLog2e))), eg = unpack(mul2(g, f2(-kLog2e)));
+  const F2 pr = add2(f2(ex2(er.x), ex2(er.y)), f2(1.0f));
+  const F2 pg = fma2(f2(ex2(eg.x), ex2(eg.y)), f2(down), f2(down));
+  const float2 P = unpack(mul2(pr, pg));
+  const F2 inv = f2(rcp(P.x), rcp(P.y));
+  c.R = mul2(pg, inv);
+  c.G = mul2(pr, inv);
+  c.t = mul2(ncs, c.R);
+  decay2<NEAR>(c.t, &c.a, &c.less);
+  const float2 v = unpack(mul2(c.less, fma2(c.a, f2(-down2), f2(-down2))));
+  c.m = f2(sqrt_ap(v.x), sqrt_ap(v.y));
+  c.b = mul2(mul2(c.m, c.G), x);
+  return c;
+}
+
+// Two channels of a row, and the same cut off for coefficients().
+template <typename T> __device__ __forceinline__ F2 gs_pair(const void *p);
+template <> __device__ __forceinline__ F2 gs_pair<float>(const void *p) {
+  const float2 v = *reinterpret_cast<const float2 *>(p);
+  return f2(v.x, v.y);
+}
+template <> __device__ __forceinline__ F2 gs_pair<__nv_bfloat16>(const void *p) {
+  const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <typename T> __device__ __forceinline__ F2 gs_clamped(const void *p);
+template <> __device__ __forceinline__ F2 gs_clamped<float>(const void *p) {
+  const float2 v = *reinterpret_cast<const float2 *>(p);
+  return f2(max_nan(v.x, -43.0f), max_nan(v.y, -43.0f));
+}
+template <> __device__ __forceinline__ F2 gs_clamped<__nv_bfloat16>(const void *p) {
+  uint32_t w;
+  asm("max.NaN.bf16x2 %0, %1, %2;"
+      : "=r"(w)
+      : "r"(*reinterpret_cast<const uint32_t *>(p)), "r"(0xc22cc22cu));
+  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 // Tensor maps and the copies they describe.
@@ -191,14 +256,47 @@ struct ContextOnce {
 bool gs_tensor_map(CUtensorMap *m, int io, const void *base, int64_t rows, int64_t L, int D,
                    int64_t ld);
 
-// Release / acquire of a flag at the GPU's scope.
-__device__ __forceinline__ void flag_set(unsigned int *p) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(1u) : "memory");
+// Records that blocks pass to one another.  A word that has not been written holds
+// kUnset, a NaN that no arithmetic gives, so that each word tells by itself whether it is
+// there: no flag, no fence, one trip to L2.
+constexpr unsigned int kUnset = 0xffffffffu;
+__device__ __forceinline__ void record_put(float4 *p, float4 v) {
+  asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y),
+               "f"(v.z), "f"(v.w)
+               : "memory");
 }
-__device__ __forceinline__ unsigned int flag_get(const unsigned int *p) {
-  unsigned int v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+__device__ __forceinline__ void record_put(float2 *p, float2 v) {
+  asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(v.x), "f"(v.y)
+               : "memory");
+}
+__device__ __forceinline__ float4 record_get(const float4 *p) {
+  float4 v;
+  asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p)
+               : "memory");
   return v;
+}
+__device__ __forceinline__ float2 record_get(const float2 *p) {
+  float2 v;
+  asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ bool is_set(float v) { return __float_as_uint(v) != kUnset; }
+__device__ __forceinline__ bool is_set(float2 v) { return is_set(v.x) && is_set(v.y); }
+__device__ __forceinline__ bool is_set(float4 v) {
+  return is_set(v.x) && is_set(v.y) && is_set(v.z) && is_set(v.w);
+}
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // The map of a state across a stretch of tokens, h_out = A h_in + H, for two channels:
