@@ -728,14 +728,14 @@ MAMBA2_API size_t mamba2_gated_scan_workspace_size(const mamba2_gated_scan_dims 
                                                    int packed) {
   if (gated_scan_dims_status(dims) != MAMBA2_OK) return 0;
   return gated_scan_workspace(gated_scan_rows(dims, packed != 0), dims->seqlen, dims->width,
-                              packed != 0);
+                              dims->io_dtype, packed != 0);
 }
 
 MAMBA2_API size_t mamba2_gated_scan_backward_workspace_size(const mamba2_gated_scan_dims *dims,
                                                             int packed) {
   if (gated_scan_dims_status(dims) != MAMBA2_OK) return 0;
   return gated_scan_backward_workspace(gated_scan_rows(dims, packed != 0), dims->seqlen,
-                                       dims->width, packed != 0);
+                                       dims->width, dims->io_dtype, packed != 0);
 }
 
 MAMBA2_API size_t mamba2_gated_scan_checkpoint_count(const mamba2_gated_scan_dims *dims,

@@ -1,17 +1,18 @@
 // Prefill and decode step of the gated linear recurrence (gated_scan.cuh).
 //
-// Prefill reads every input once.  A tile is 64 tokens of 64 channels of a row;
-// resident blocks take tiles in order, all channels of a stretch of tokens before the
-// next stretch, from a counter:
+// Prefill reads every input once.  A tile is 128 (fp32: 64) tokens of 64 channels of a
+// row; resident blocks take tiles in order, all channels of a stretch of tokens before
+// the next stretch, from a counter:
 //   1. the tile's x, r and g arrive by TMA, two tiles ahead of the arithmetic;
-//   2. each thread of the eight computing warps turns the 8 tokens of its two channels
-//      into h_t = a_t h_{t-1} + b_t, keeps a and b in registers, and composes them
-//      into the map of its segment, (A, H), in shared memory;
-//   3. meanwhile a ninth warp looks up the state entering the tile: it folds the
-//      maps of the tiles before it onto the state that the group of tiles before left.
-//      When the segments are there it publishes the tile's own map and fetches the
-//      tile after next;
-//   4. each thread runs its tokens from that state and writes y.
+//   2. each thread of the eight computing warps turns the 16 (8) tokens of its two
+//      channels into h_t = a_t h_{t-1} + b_t, keeps a and b in registers, and composes
+//      them into the map of its segment, (A, H), in shared memory; the last of the
+//      warps publishes the whole tile's map;
+//   3. meanwhile a ninth warp looks up the state entering the tile: it folds the maps of
+//      the tiles before it onto the state that one further back left.  When the
+//      segments are there it fetches the tile after next;
+//   4. each thread runs its tokens from that state and writes y; the last of the warps
+//      has published the state that the tile leaves.
 // Nothing makes the whole block wait: warps meet at mbarriers only.  Every state is put
 // together in an order fixed by the tiles' numbers alone, so that results do not depend
 // on timing.  A block waits only for tiles of lower numbers, whose blocks are running:
@@ -27,32 +28,40 @@ static __device__ unsigned int g_gs_stall = 0;  // mamba2_debug_stall_waits
 
 namespace {
 
-constexpr int kTile = 64;   // tokens of a tile
 constexpr int kWidth = 64;  // channels of a tile: two for each lane
-constexpr int kWarps = 8;   // that compute
-constexpr int kTokens = kTile / kWarps;  // of a thread
+constexpr int kWarps = 4;   // that compute
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kStages = 2;
-static_assert(kGsChunk % kTile == 0, "checkpoints lie between tiles");
-// Tiles whose maps are folded one by one before a state is published again: more
-// make a tile read more maps, fewer lengthen the chain of states.
-constexpr int kGroup = 8;
+// The state entering a tile is put together from that left by the `back`th tile before
+// it and the maps of those between, one after the other: E(t + 1) = A(t) E(t) + H(t),
+// rounded the same whatever `back` is.  8 where a step has many tiles (that state is then
+// there, and only the maps of tiles under way are waited for); 32 where a narrow row's
+// tiles are nearly all under way at once, for a chain of fewer links.
+constexpr int kNear = 8, kFar = 32;
+constexpr int kFarBelow = 24;  // tiles of a step
+constexpr int kBatch = 8;      // maps read at once
+
+// Blocks on an SM at once: what shared memory holds.
+template <bool GATED> constexpr int kResident = GATED ? 3 : 4;
+// Tokens of a tile: what the registers of a block's threads and the shared memory of
+// two blocks to an SM hold.
+template <typename T> constexpr int kTile = sizeof(T) == 2 ? 64 : 32;
+template <typename T> constexpr int kTokens = kTile<T> / kWarps;  // of a thread
 
 // Bits of a token's mark in packed rows: (sequence << 2) | last << 1 | first.
 constexpr int kFirst = 1, kLast = 2;
 
 struct Scan {
-  const float *ncs;  // [D] -c softplus(lam) log2(e)
-  const void *z;
-  int64_t ld_z, L;
-  int D, nblk, steps, rows, tiles;  // steps: tiles along a row's tokens
+  const float *ncs;  // [nblk][64] -c softplus(lam) log2(e)
+  int64_t L;
+  int D, nblk, steps, rows, tiles, back;  // steps: tiles along a row's tokens
   const int *marks;         // packed rows: [L], else null
   const unsigned int *bad;  // packed rows: wrong offsets
   void *y;                  // or null: only the states entering the chunks are wanted
   const float *h_in;        // or null
   float *h_out, *ck;        // or null
-  float4 *maps;             // [tiles][32]
-  float2 *states;           // [groups][rows][nblk][32]
+  float4 *maps;             // [tiles][32]: the tiles' maps
+  float2 *states;           // [tiles][32]: the states they leave
   unsigned int *ticket;
 };
 
@@ -60,11 +69,13 @@ struct Tile {
   int cb, row, step, left;
 };
 
-template <typename T> struct Shared {
+template <typename T, bool GATED> struct Shared {
+  static constexpr int kTensors = GATED ? 4 : 3;
   static constexpr int kRow = kWidth * (int)sizeof(T);  // bytes of a token
-  static constexpr int kTensor = kTile * kRow;
-  alignas(128) unsigned char in[kStages][3 * kTensor];
-  alignas(16) int marks[kStages][kTile];
+  static constexpr int kTensor = kTile<T> * kRow;
+  alignas(128) unsigned char in[kStages][kTensors * kTensor];
+  alignas(16) int marks[kStages][kTile<T>];
+  alignas(16) float ncs[kStages][kWidth];
   float4 seg[2][kWarps][32];
   float2 enter[2][32];
   uint64_t full[kStages], segs[2], entered[2];
@@ -80,7 +91,8 @@ __global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, uin
   launch_dependents();
   const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t all = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = at; i < D; i += all) ncs[i] = -c * softplus_f(lam[i]) * kLog2e;
+  for (int64_t i = at; i < (D + kWidth - 1) / kWidth * kWidth; i += all)
+    ncs[i] = i < D ? -c * softplus_f(lam[i]) * kLog2e : 0.0f;
   for (int64_t i = at; i < nrecords; i += all)
     records[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
   if (at == 0) *ticket = 0;
@@ -113,13 +125,13 @@ __global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, uin
 // Step 2: a and b of the thread's tokens, and their composition.
 template <typename T, bool FULL, bool PACKED, bool NEAR>
 __device__ __forceinline__ float4 make_maps(const unsigned char *in, const int *marks, F2 ncs, int n,
-                                            const Scan &p, int d, F2 (&a)[kTokens],
-                                            F2 (&b)[kTokens]) {
-  constexpr int kRow = Shared<T>::kRow, kTensor = Shared<T>::kTensor;
+                                            const Scan &p, int d, F2 (&a)[kTokens<T>],
+                                            F2 (&b)[kTokens<T>]) {
+  constexpr int kRow = Shared<T, false>::kRow, kTensor = Shared<T, false>::kTensor;
   F2 A = f2(1.0f), H = f2(0.0f);
   float4 map = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < kTokens; ++i) {
+  for (int i = 0; i < kTokens<T>; ++i) {
     const unsigned char *row = in + i * kRow;
     const Coeffs c =
         coefficients<NEAR>(gs_pair<T>(row), gs_clamped<T>(row + kTensor),
@@ -158,11 +170,12 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16 *p, float2 v) {
   *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
 }
 
-// Step 3: the ninth warp.
-template <typename T, bool PACKED>
-__device__ __forceinline__ void look_up(Shared<T> &sm, const CUtensorMap &map_x,
+// The ninth warp: step 3, and the copies of step 1.
+template <typename T, bool PACKED, bool GATED>
+__device__ __forceinline__ void look_up(Shared<T, GATED> &sm, const CUtensorMap &map_x,
                                         const CUtensorMap &map_r, const CUtensorMap &map_g,
-                                        const Scan &p) {
+                                        const CUtensorMap &map_z, const Scan &p) {
+  using S = Shared<T, GATED>;
   const int lane = threadIdx.x & 31;
   const int per_step = p.rows * p.nblk;
   // one lane: tile t's copies, into stage s
@@ -177,14 +190,16 @@ __device__ __forceinline__ void look_up(Shared<T> &sm, const CUtensorMap &map_x,
       mbar_arrive(&sm.full[s]);
       return;
     }
-    const int t0 = q.step * kTile, n = (int)min((int64_t)kTile, p.L - t0);
+    const int t0 = q.step * kTile<T>, n = (int)min((int64_t)kTile<T>, p.L - t0);
     // (whole 16-byte groups of marks; the array is padded)
     const uint32_t mark_bytes = PACKED ? (n * 4 + 15) / 16 * 16 : 0;
-    mbar_arrive_expect_tx(&sm.full[s], 3 * Shared<T>::kTensor + mark_bytes);
+    mbar_arrive_expect_tx(&sm.full[s], S::kTensors * S::kTensor + kWidth * 4 + mark_bytes);
     unsigned char *in = sm.in[s];
     tma_load_3d(in, &map_x, q.cb * kWidth, t0, q.row, &sm.full[s]);
-    tma_load_3d(in + Shared<T>::kTensor, &map_r, q.cb * kWidth, t0, q.row, &sm.full[s]);
-    tma_load_3d(in + 2 * Shared<T>::kTensor, &map_g, q.cb * kWidth, t0, q.row, &sm.full[s]);
+    tma_load_3d(in + S::kTensor, &map_r, q.cb * kWidth, t0, q.row, &sm.full[s]);
+    tma_load_3d(in + 2 * S::kTensor, &map_g, q.cb * kWidth, t0, q.row, &sm.full[s]);
+    if (GATED) tma_load_3d(in + 3 * S::kTensor, &map_z, q.cb * kWidth, t0, q.row, &sm.full[s]);
+    bulk_g2s(sm.ncs[s], p.ncs + q.cb * kWidth, kWidth * 4, &sm.full[s]);
     if (PACKED) bulk_g2s(sm.marks[s], p.marks + t0, mark_bytes, &sm.full[s]);
   };
   if (lane == 0)
@@ -198,95 +213,83 @@ __device__ __forceinline__ void look_up(Shared<T> &sm, const CUtensorMap &map_x,
     if (q.left <= 0) return;  // so is every later tile's: no copy is under way
     int next = 0;
     if (lane == 0) next = (int)atomicAdd(p.ticket, 1u);  // wanted when the segments are there
-    const int d = q.cb * kWidth + 2 * lane, mine = q.row * p.nblk + q.cb;
-    const int tile = q.step * per_step + mine;
-    const int group = q.step / kGroup, in_group = q.step % kGroup;
-    const bool last = q.step == p.steps - 1;
-    bool published = false, entered = false, based = group == 0;
-    int folded = 0;  // maps of the group's tiles before this one, and their base
-    const float2 *base = p.states + ((int64_t)(group - 1) * per_step + mine) * 32 + lane;
-    const float4 *before = p.maps + ((int64_t)group * kGroup * per_step + mine) * 32 + lane;
+    const int d = q.cb * kWidth + 2 * lane;
+    const int tile = q.step * per_step + q.row * p.nblk + q.cb;
+    const int between = min(q.step, p.back - 1);
+    bool fetched = false, entered = false, based = q.step < p.back;
+    int folded = 0;  // maps, of those between
+    const float2 *base = p.states + ((int64_t)tile - (int64_t)p.back * per_step) * 32 + lane;
+    const float4 *maps = p.maps + ((int64_t)tile - (int64_t)between * per_step) * 32 + lane;
     float2 h = make_float2(0.0f, 0.0f);
     if (!PACKED && q.step == 0 && p.h_in != nullptr && d < p.D)
       h = *reinterpret_cast<const float2 *>(p.h_in + (int64_t)q.row * p.D + d);
-    float4 map;
     unsigned long long since = 0;
     for (;;) {
-      if (!published &&
-          __all_sync(0xffffffffu, entered ? mbar_try_wait(&sm.segs[half], phase)
-                                          : mbar_test(&sm.segs[half], phase))) {
-        map = sm.seg[half][0][lane];
-#pragma unroll
-        for (int k = 1; k < kWarps; ++k) map = gs_then(map, sm.seg[half][k][lane]);
-        if (q.step == 0) {  // known whole: nothing before it counts
-          const float2 e = gs_through(map, h);
-          map = make_float4(-0.0f, -0.0f, e.x, e.y);
-        }
-        if (!last && in_group != kGroup - 1) record_put(p.maps + (int64_t)tile * 32 + lane, map);
-        if (lane == 0) fetch(s, next);
-        __syncwarp();
-        published = true;
-      }
       if (!entered) {
         float2 b = make_float2(0.0f, 0.0f);
-        float4 m[kGroup - 1];
+        float4 m[kBatch];
         if (!based) b = record_get(base);
-        unsigned int there = 0;
 #pragma unroll
-        for (int k = 0; k < kGroup - 1; ++k)
-          if (k >= folded && k < in_group) m[k] = record_get(before + (int64_t)k * per_step * 32);
+        for (int k = 0; k < kBatch; ++k)
+          if (folded + k < between) m[k] = record_get(maps + (int64_t)(folded + k) * per_step * 32);
+        unsigned int there = based || is_set(b) ? 1u << 31 : 0u;
 #pragma unroll
-        for (int k = 0; k < kGroup - 1; ++k)
-          if (k < folded || k >= in_group || is_set(m[k])) there |= 1u << k;
-        if (based || is_set(b)) there |= 1u << 31;
+        for (int k = 0; k < kBatch; ++k)
+          if (folded + k < between && is_set(m[k])) there |= 1u << k;
         there = __reduce_and_sync(0xffffffffu, there);
         if (there >> 31) {
           if (!based) h = b;
           based = true;
+          const int run = __ffs(~there) - 1;  // maps there without a gap
 #pragma unroll
-          for (int k = 0; k < kGroup - 1; ++k)
-            if (k == folded && k < in_group && (there >> k & 1)) {
-              h = gs_through(m[k], h);
-              ++folded;
-            }
-          entered = folded == in_group;
+          for (int k = 0; k < kBatch; ++k)
+            if (k < run) h = gs_through(m[k], h);
+          folded += run;
+          entered = folded == between;
         }
         if (entered) {
           sm.enter[half][lane] = h;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.entered[half]);
-          if (p.ck != nullptr && q.step % (kGsChunk / kTile) == 0 && d < p.D) {
+          constexpr int kPer = kGsChunk / kTile<T>;
+          if (p.ck != nullptr && q.step % kPer == 0 && d < p.D) {
             const int64_t nch = (p.L + kGsChunk - 1) / kGsChunk;
-            *reinterpret_cast<float2 *>(
-                p.ck + ((int64_t)q.row * nch + q.step / (kGsChunk / kTile)) * p.D + d) = h;
+            *reinterpret_cast<float2 *>(p.ck + ((int64_t)q.row * nch + q.step / kPer) * p.D + d) =
+                h;
           }
         }
       }
-      if (published && entered) break;
+      if (!fetched && __all_sync(0xffffffffu, entered ? mbar_try_wait(&sm.segs[half], phase)
+                                                      : mbar_test(&sm.segs[half], phase))) {
+        if (lane == 0) fetch(s, next);  // every warp is done with the stage
+        __syncwarp();
+        fetched = true;
+      }
+      if (fetched && entered) break;
       const unsigned long long now = globaltimer_ns();
       if (since == 0) since = now;
       if (__any_sync(0xffffffffu, now - since > kWaitLimitNs)) {
         // what this block has under way lands before the warp leaves
         if (lane == 0) {
           atomicOr(&g_gs_errors, kErrWaitTimeout);
-          for (int i = it + published; i < it + published + kStages; ++i)
+          for (int i = it + fetched; i < it + fetched + kStages; ++i)
             mbar_wait_bounded(&sm.full[i % kStages], (i / kStages) & 1, &g_gs_errors);
         }
         return;
       }
     }
-    if (!last && in_group == kGroup - 1)
-      record_put(p.states + ((int64_t)group * per_step + mine) * 32 + lane, gs_through(map, h));
   }
 }
 
 template <typename T, bool PACKED, bool GATED>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, kResident<GATED>)
     gs_prefill_kernel(const __grid_constant__ CUtensorMap map_x,
                       const __grid_constant__ CUtensorMap map_r,
-                      const __grid_constant__ CUtensorMap map_g, const Scan p) {
+                      const __grid_constant__ CUtensorMap map_g,
+                      const __grid_constant__ CUtensorMap map_z, const Scan p) {
   extern __shared__ __align__(128) unsigned char raw[];
-  Shared<T> &sm = *reinterpret_cast<Shared<T> *>(raw);
+  using S = Shared<T, GATED>;
+  S &sm = *reinterpret_cast<S *>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (test_stall(&g_gs_stall, &g_gs_errors)) return;
   if (threadIdx.x == 0) {
@@ -301,63 +304,69 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
   grid_dependency_wait();
   if (PACKED && *p.bad) return;
   if (warp == kWarps) {
-    look_up<T, PACKED>(sm, map_x, map_r, map_g, p);
+    look_up<T, PACKED, GATED>(sm, map_x, map_r, map_g, map_z, p);
     return;
   }
 
-  const int first = warp * kTokens;
+  const int first = warp * kTokens<T>;
   for (int it = 0;; ++it) {
     const int s = it % kStages, half = it & 1;
     const uint32_t phase = (it >> 1) & 1;
     if (!mbar_wait_bounded(&sm.full[s], (it / kStages) & 1, &g_gs_errors)) return;
     const Tile q = sm.tile[s];
     if (q.left <= 0) return;
-    const int t0 = q.step * kTile, n = (int)min((int64_t)kTile, p.L - t0);
+    const int t0 = q.step * kTile<T>, n = (int)min((int64_t)kTile<T>, p.L - t0);
     const int d = q.cb * kWidth + 2 * lane;
     const bool real = d < p.D;
-    float2 ncs = make_float2(0.0f, 0.0f);
-    if (real) ncs = *reinterpret_cast<const float2 *>(p.ncs + d);
-    F2 a[kTokens], b[kTokens];
-    const unsigned char *in = sm.in[s] + first * Shared<T>::kRow + lane * (2 * (int)sizeof(T));
+    const float2 ncs = *reinterpret_cast<const float2 *>(&sm.ncs[s][2 * lane]);
+    F2 a[kTokens<T>], b[kTokens<T>];
+    const unsigned char *in = sm.in[s] + first * S::kRow + lane * (2 * (int)sizeof(T));
     const int *marks = sm.marks[s] + first;
     const F2 k = f2(ncs.x, ncs.y);
     float4 map;
     if (__all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f))
-      map = n == kTile ? make_maps<T, true, PACKED, true>(in, marks, k, n - first, p, d, a, b)
-                       : make_maps<T, false, PACKED, true>(in, marks, k, n - first, p, d, a, b);
+      map = n == kTile<T> ? make_maps<T, true, PACKED, true>(in, marks, k, n - first, p, d, a, b)
+                          : make_maps<T, false, PACKED, true>(in, marks, k, n - first, p, d, a, b);
     else
       map = make_maps<T, false, PACKED, false>(in, marks, k, n - first, p, d, a, b);
     sm.seg[half][warp][lane] = map;
     int ends = 0;  // packed rows: which of the thread's tokens end a sequence
     if (PACKED && p.h_out != nullptr) {
 #pragma unroll
-      for (int i = 0; i < kTokens; ++i)
+      for (int i = 0; i < kTokens<T>; ++i)
         if (i < n - first && (marks[i] & kLast)) ends |= 1 << i;
+    }
+    typename Pair<T>::V gate[GATED ? kTokens<T> : 1];
+    if (GATED) {
+#pragma unroll
+      for (int i = 0; i < kTokens<T>; ++i)
+        gate[i] = *reinterpret_cast<const typename Pair<T>::V *>(in + i * S::kRow + 3 * S::kTensor);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.segs[half]);
     const int64_t token = (int64_t)q.row * p.L + t0 + first;
-    typename Pair<T>::V gate[GATED ? kTokens : 1];  // under way while the state is looked up
-    if (GATED) {
-      const T *z = static_cast<const T *>(p.z) + token * p.ld_z + d;
-#pragma unroll
-      for (int i = 0; i < kTokens; ++i) {
-        gate[i] = Pair<T>::put(0.0f, 0.0f);
-        if (real && i < n - first)
-          gate[i] = *reinterpret_cast<const typename Pair<T>::V *>(z + i * p.ld_z);
-      }
+    if (!mbar_wait_bounded(&sm.segs[half], phase, &g_gs_errors)) return;
+    // the segments before this one as one map
+    float4 pre = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+    for (int k = 0; k < warp; ++k) pre = gs_then(pre, sm.seg[half][k][lane]);
+    const int tile = (q.step * p.rows + q.row) * p.nblk + q.cb;
+    const bool tells = warp == kWarps - 1 && q.step < p.steps - 1;
+    if (tells) map = gs_then(pre, map);  // of the tile
+    if (tells && q.step > 0) record_put(p.maps + (int64_t)tile * 32 + lane, map);
+    if (!mbar_wait_bounded(&sm.entered[half], phase, &g_gs_errors)) return;
+    const float2 enter = sm.enter[half][lane];
+    if (tells) {
+      const float2 leave = gs_through(map, enter);
+      record_put(p.states + (int64_t)tile * 32 + lane, leave);
+      if (q.step == 0)  // known whole: nothing before it counts
+        record_put(p.maps + (int64_t)tile * 32 + lane,
+                   make_float4(-0.0f, -0.0f, leave.x, leave.y));
     }
-    if (!mbar_wait_bounded(&sm.segs[half], phase, &g_gs_errors) ||
-        !mbar_wait_bounded(&sm.entered[half], phase, &g_gs_errors))
-      return;
-    if (p.y == nullptr) continue;
-
-    float2 h = sm.enter[half][lane];
-    for (int k = 0; k < warp; ++k) h = gs_through(sm.seg[half][k][lane], h);
+    const float2 h = gs_through(pre, enter);
     F2 hh = f2(h.x, h.y);
     T *y = static_cast<T *>(p.y) + token * p.D + d;
 #pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
+    for (int i = 0; i < kTokens<T>; ++i) {
       if (PACKED) {
         const float2 ai = unpack(a[i]), bi = unpack(b[i]), hi = unpack(hh);
         const float2 e = gs_through(make_float4(ai.x, ai.y, bi.x, bi.y), hi);
@@ -365,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
       } else {
         hh = fma2(a[i], hh, b[i]);
       }
-      if (real && i < n - first) {
+      if (p.y != nullptr && real && i < n - first) {
         F2 o = hh;
         if (GATED) {
           const float2 z = Pair<T>::get(gate[i]);
@@ -378,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
       }
     }
     if (!PACKED && p.h_out != nullptr && q.step == p.steps - 1 && real && first < n &&
-        n <= first + kTokens)
+        n <= first + kTokens<T>)
       // (tokens behind the last leave the state as it is)
       *reinterpret_cast<float2 *>(p.h_out + (int64_t)q.row * p.D + d) = unpack(hh);
   }
@@ -423,19 +432,19 @@ template <typename T> In<T> inputs(const GatedScanArgs &a) {
 // Where the parts of the workspace are.
 struct Plan {
   int nblk, steps;
-  int64_t tiles, groups;
+  int64_t tiles;
   size_t ncs, maps, states, marks, total;
 };
-Plan plan_of(int64_t rows, int64_t L, int D, bool packed) {
+Plan plan_of(int64_t rows, int64_t L, int D, int io, bool packed) {
   Plan p;
   p.nblk = (int)ceil_div(D, kWidth);
-  p.steps = (int)ceil_div(L, kTile);
+  p.steps = (int)ceil_div(L, io == MAMBA2_BF16 ? kTile<__nv_bfloat16> : kTile<float>);
   p.tiles = rows * p.steps * p.nblk;
-  p.groups = p.steps / kGroup;
+  const size_t records = p.steps > 1 ? (size_t)p.tiles * 32 : 0;
   p.ncs = 256;  // after the counter and the flag of wrong offsets
-  p.maps = p.ncs + align_up((size_t)D * 4, 256);
-  p.states = p.maps + (p.steps > 1 ? (size_t)p.tiles * 32 * 16 : 0);
-  p.marks = p.states + (size_t)(p.groups * rows * p.nblk) * 32 * 8;
+  p.maps = p.ncs + align_up((size_t)p.nblk * kWidth * 4, 256);
+  p.states = p.maps + records * 16;
+  p.marks = p.states + records * 8;
   p.total = p.marks + (packed ? align_up((size_t)L * 4, 256) : 0);
   return p;
 }
@@ -449,10 +458,9 @@ int sm_count() {
 }
 
 template <typename T, bool PACKED, bool GATED>
-cudaError_t launch(const GatedScanArgs &a, const CUtensorMap (&m)[3], const Scan &p) {
-  constexpr size_t smem = sizeof(Shared<T>);
-  constexpr int kResident = sizeof(T) == 2 ? 3 : 2;
-  static_assert(kResident * (smem + 2048) <= 227 * 1024, "blocks to an SM");
+cudaError_t launch(const GatedScanArgs &a, const CUtensorMap (&m)[4], const Scan &p) {
+  constexpr size_t smem = sizeof(Shared<T, GATED>);
+  static_assert(kResident<GATED> * (smem + 1024 + 256) <= 228 * 1024, "blocks to an SM");
   static ContextOnce once;
   if (!once.done()) {
     const cudaError_t e = cudaFuncSetAttribute(
@@ -461,7 +469,7 @@ cudaError_t launch(const GatedScanArgs &a, const CUtensorMap (&m)[3], const Scan
     once.set();
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min(p.tiles, kResident * sm_count()), 1, 1);
+  cfg.gridDim = dim3((unsigned)std::min(p.tiles, kResident<GATED> * sm_count()), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = a.stream;
@@ -470,23 +478,22 @@ cudaError_t launch(const GatedScanArgs &a, const CUtensorMap (&m)[3], const Scan
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gs_prefill_kernel<T, PACKED, GATED>, m[0], m[1], m[2], p);
+  return cudaLaunchKernelEx(&cfg, gs_prefill_kernel<T, PACKED, GATED>, m[0], m[1], m[2], m[3], p);
 }
 
 template <typename T> cudaError_t prefill(const GatedScanArgs &a) {
   const int64_t rows = a.rows();
   const bool packed = a.cu != nullptr;
-  const Plan w = plan_of(rows, a.L, a.D, packed);
+  const Plan w = plan_of(rows, a.L, a.D, a.io, packed);
   Scan p;
   p.ncs = reinterpret_cast<float *>(a.ws + w.ncs);
-  p.z = a.z;
-  p.ld_z = a.ld_z;
   p.L = a.L;
   p.D = a.D;
   p.nblk = w.nblk;
   p.steps = w.steps;
   p.rows = (int)rows;
   p.tiles = (int)w.tiles;
+  p.back = rows * w.nblk < kFarBelow ? kFar : kNear;
   p.marks = packed ? reinterpret_cast<int *>(a.ws + w.marks) : nullptr;
   p.ticket = reinterpret_cast<unsigned int *>(a.ws);
   p.bad = p.ticket + 1;
@@ -496,10 +503,12 @@ template <typename T> cudaError_t prefill(const GatedScanArgs &a) {
   p.ck = a.ck;
   p.maps = reinterpret_cast<float4 *>(a.ws + w.maps);
   p.states = reinterpret_cast<float2 *>(a.ws + w.states);
-  CUtensorMap m[3];
+  const bool gated = a.z != nullptr && a.y != nullptr;
+  CUtensorMap m[4];
   if (!gs_tensor_map(&m[0], a.io, a.x, rows, a.L, a.D, a.ld_x) ||
       !gs_tensor_map(&m[1], a.io, a.r, rows, a.L, a.D, a.ld_r) ||
-      !gs_tensor_map(&m[2], a.io, a.g, rows, a.L, a.D, a.ld_g))
+      !gs_tensor_map(&m[2], a.io, a.g, rows, a.L, a.D, a.ld_g) ||
+      !gs_tensor_map(&m[3], a.io, gated ? a.z : a.x, rows, a.L, a.D, gated ? a.ld_z : a.ld_x))
     return cudaErrorInvalidValue;
   const int64_t nrecords = (int64_t)(w.marks - w.maps) / 16;  // maps and states, side by side
   const int64_t work = std::max(std::max<int64_t>(a.D, nrecords), packed ? a.L : 0);
@@ -509,7 +518,6 @@ template <typename T> cudaError_t prefill(const GatedScanArgs &a) {
       const_cast<unsigned int *>(p.bad), p.h_out, a.states_in);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const bool gated = a.z != nullptr && a.y != nullptr;
   if (packed) e = gated ? launch<T, true, true>(a, m, p) : launch<T, true, false>(a, m, p);
   else e = gated ? launch<T, false, true>(a, m, p) : launch<T, false, false>(a, m, p);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -563,7 +571,8 @@ bool gs_tensor_map(CUtensorMap *m, int io, const void *base, int64_t rows, int64
   const uint64_t esz = bf ? 2 : 4;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)L, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {(uint64_t)ld * esz, (uint64_t)ld * esz * (uint64_t)L};
-  const cuuint32_t box[3] = {(cuuint32_t)kWidth, (cuuint32_t)kTile, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)kWidth,
+                              (cuuint32_t)(bf ? kTile<__nv_bfloat16> : kTile<float>), 1};
   const cuuint32_t one[3] = {1, 1, 1};
   return encode(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
                 const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -571,8 +580,8 @@ bool gs_tensor_map(CUtensorMap *m, int io, const void *base, int64_t rows, int64
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t gated_scan_workspace(int64_t rows, int64_t L, int D, bool packed) {
-  return plan_of(rows, L, D, packed).total;
+size_t gated_scan_workspace(int64_t rows, int64_t L, int D, int io, bool packed) {
+  return plan_of(rows, L, D, io, packed).total;
 }
 
 cudaError_t gated_scan_prefill(const GatedScanArgs &a) {

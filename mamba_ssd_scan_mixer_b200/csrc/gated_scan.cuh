@@ -47,10 +47,10 @@ struct GatedScanBackwardArgs {
 };
 
 cudaError_t gated_scan_prefill(const GatedScanArgs &a);
-size_t gated_scan_workspace(int64_t rows, int64_t L, int D, bool packed);
+size_t gated_scan_workspace(int64_t rows, int64_t L, int D, int io, bool packed);
 cudaError_t gated_scan_step(const GatedScanArgs &a);
 cudaError_t gated_scan_backward(const GatedScanBackwardArgs &a);
-size_t gated_scan_backward_workspace(int64_t rows, int64_t L, int D, bool packed);
+size_t gated_scan_backward_workspace(int64_t rows, int64_t L, int D, int io, bool packed);
 cudaError_t take_gated_scan_errors(unsigned int *out);
 cudaError_t set_gated_scan_stall(unsigned int v);
 // Sets *bad to whether the offsets of packed rows are wrong (and raises the flag).

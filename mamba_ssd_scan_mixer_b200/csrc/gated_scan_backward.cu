@@ -265,9 +265,9 @@ template <typename T> cudaError_t backward(const GatedScanBackwardArgs &b) {
 
 }  // namespace
 
-size_t gated_scan_backward_workspace(int64_t rows, int64_t L, int D, bool packed) {
+size_t gated_scan_backward_workspace(int64_t rows, int64_t L, int D, int io, bool packed) {
   const size_t n = (size_t)rows * (size_t)ceil_div(L, kGsChunk) * (size_t)D;
-  return 256 + align_up(5 * n * 4, 256) + gated_scan_workspace(rows, L, D, packed);
+  return 256 + align_up(5 * n * 4, 256) + gated_scan_workspace(rows, L, D, io, packed);
 }
 
 cudaError_t gated_scan_backward(const GatedScanBackwardArgs &b) {
