@@ -18,6 +18,7 @@
 // on timing.  A block waits only for tiles of lower numbers, whose blocks are running:
 // the tiles are handed out in order.
 #include <algorithm>
+#include <type_traits>
 
 #include "gated_scan.cuh"
 
@@ -78,8 +79,9 @@ template <typename T, bool GATED> struct Shared {
   alignas(16) float ncs[kStages][kWidth];
   float4 seg[2][kWarps][32];
   float2 enter[2][32];
-  uint64_t full[kStages], segs[2], entered[2];
+  uint64_t full[kStages], segs[2];
   Tile tile[kStages];
+  int dead;  // a wait ran out: everybody leaves after the next `entered`
 };
 
 // The counter and the records reset, the decays' factor per channel, and for packed rows the
@@ -122,14 +124,26 @@ __global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, uin
         for (int d = threadIdx.x % 32; d < D; d += 32) h_out[s * D + d] = 0.0f;
 }
 
-// Step 2: a and b of the thread's tokens, and their composition.
-template <typename T, bool FULL, bool PACKED, bool NEAR>
-__device__ __forceinline__ float4 make_maps(const unsigned char *in, const int *marks, F2 ncs, int n,
-                                            const Scan &p, int d, F2 (&a)[kTokens<T>],
-                                            F2 (&b)[kTokens<T>]) {
+// The block's named barriers.  All wait in hardware: warps that ask an mbarrier again and
+// again took a third of the instructions issued.
+__device__ __forceinline__ void segments_done() {  // the computing warps
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+}
+__device__ __forceinline__ void entered_wait(int half) {  // the computing warps, for the ninth
+  asm volatile("bar.sync %0, %1;" ::"r"(2 + half), "n"(kThreads) : "memory");
+}
+__device__ __forceinline__ void entered_signal(int half) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(2 + half), "n"(kThreads) : "memory");
+}
+
+// Step 2: a and b of the thread's tokens, and their composition.  `begins`: the tokens (a
+// bit each) that begin a sequence of packed rows.
+template <typename T, bool FULL, bool RESETS, bool NEAR>
+__device__ __forceinline__ float4 make_maps(const unsigned char *in, const int *marks,
+                                            unsigned int begins, F2 ncs, int n, const Scan &p,
+                                            int d, F2 (&a)[kTokens<T>], F2 (&b)[kTokens<T>]) {
   constexpr int kRow = Shared<T, false>::kRow, kTensor = Shared<T, false>::kTensor;
   F2 A = f2(1.0f), H = f2(0.0f);
-  float4 map = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
 #pragma unroll
   for (int i = 0; i < kTokens<T>; ++i) {
     const unsigned char *row = in + i * kRow;
@@ -142,23 +156,19 @@ __device__ __forceinline__ float4 make_maps(const unsigned char *in, const int *
       a[i] = f2(1.0f);
       b[i] = f2(0.0f);
     }
-    if (PACKED) {
-      if ((FULL || i < n) && (marks[i] & kFirst)) {
-        if (p.h_in != nullptr && d < p.D) {
-          const float2 h =
-              *reinterpret_cast<const float2 *>(p.h_in + (int64_t)(marks[i] >> 2) * p.D + d);
-          b[i] = fma2(a[i], f2(h.x, h.y), b[i]);
-        }
-        a[i] = f2(-0.0f);
+    if (RESETS && (begins >> i & 1)) {
+      if (p.h_in != nullptr && d < p.D) {
+        const float2 h =
+            *reinterpret_cast<const float2 *>(p.h_in + (int64_t)(marks[i] >> 2) * p.D + d);
+        b[i] = fma2(a[i], f2(h.x, h.y), b[i]);
       }
-      const float2 ai = unpack(a[i]), bi = unpack(b[i]);
-      map = gs_then(map, make_float4(ai.x, ai.y, bi.x, bi.y));
+      A = f2(-0.0f);
+      H = b[i];
     } else {
       A = mul2(A, a[i]);
       H = fma2(a[i], H, b[i]);
     }
   }
-  if (PACKED) return map;
   const float2 x = unpack(A), y = unpack(H);
   return make_float4(x.x, x.y, y.x, y.y);
 }
@@ -202,8 +212,13 @@ __device__ __forceinline__ void look_up(Shared<T, GATED> &sm, const CUtensorMap 
     bulk_g2s(sm.ncs[s], p.ncs + q.cb * kWidth, kWidth * 4, &sm.full[s]);
     if (PACKED) bulk_g2s(sm.marks[s], p.marks + t0, mark_bytes, &sm.full[s]);
   };
-  if (lane == 0)
-    for (int s = 0; s < kStages; ++s) fetch(s, (int)atomicAdd(p.ticket, 1u));
+  if (lane == 0) {
+    fetch(0, (int)atomicAdd(p.ticket, 1u));
+    // by then the other blocks have their first tile too: no block holds two neighbours
+    // that it would work on one after the other while others wait for the second
+    mbar_wait_parked(&sm.full[0], 0, &g_gs_errors);
+    fetch(1, (int)atomicAdd(p.ticket, 1u));
+  }
   __syncwarp();
 
   for (int it = 0;; ++it) {
@@ -249,8 +264,7 @@ __device__ __forceinline__ void look_up(Shared<T, GATED> &sm, const CUtensorMap 
         }
         if (entered) {
           sm.enter[half][lane] = h;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.entered[half]);
+          entered_signal(half);
           constexpr int kPer = kGsChunk / kTile<T>;
           if (p.ck != nullptr && q.step % kPer == 0 && d < p.D) {
             const int64_t nch = (p.L + kGsChunk - 1) / kGsChunk;
@@ -269,7 +283,10 @@ __device__ __forceinline__ void look_up(Shared<T, GATED> &sm, const CUtensorMap 
       const unsigned long long now = globaltimer_ns();
       if (since == 0) since = now;
       if (__any_sync(0xffffffffu, now - since > kWaitLimitNs)) {
-        // what this block has under way lands before the warp leaves
+        // what this block has under way lands before the warp leaves, and nobody waits for it
+        sm.dead = 1;
+        __syncwarp();
+        entered_signal(entered ? half ^ 1 : half);
         if (lane == 0) {
           atomicOr(&g_gs_errors, kErrWaitTimeout);
           for (int i = it + fetched; i < it + fetched + kStages; ++i)
@@ -296,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
     for (int s = 0; s < kStages; ++s) mbar_init(&sm.full[s], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.segs[s], kWarps);
-      mbar_init(&sm.entered[s], 1);
     }
+    sm.dead = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -311,8 +328,7 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
   const int first = warp * kTokens<T>;
   for (int it = 0;; ++it) {
     const int s = it % kStages, half = it & 1;
-    const uint32_t phase = (it >> 1) & 1;
-    if (!mbar_wait_bounded(&sm.full[s], (it / kStages) & 1, &g_gs_errors)) return;
+    if (!mbar_wait_parked(&sm.full[s], (it / kStages) & 1, &g_gs_errors)) sm.dead = 1;
     const Tile q = sm.tile[s];
     if (q.left <= 0) return;
     const int t0 = q.step * kTile<T>, n = (int)min((int64_t)kTile<T>, p.L - t0);
@@ -322,20 +338,22 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
     F2 a[kTokens<T>], b[kTokens<T>];
     const unsigned char *in = sm.in[s] + first * S::kRow + lane * (2 * (int)sizeof(T));
     const int *marks = sm.marks[s] + first;
+    // packed rows: which of the warp's tokens begin and end a sequence
+    unsigned int begins = 0, ends = 0;
+    if (PACKED) {
+      const int mark = lane < min(kTokens<T>, n - first) ? marks[lane] : 0;
+      begins = __ballot_sync(0xffffffffu, mark & kFirst);
+      ends = __ballot_sync(0xffffffffu, p.h_out != nullptr && (mark & kLast));
+    }
     const F2 k = f2(ncs.x, ncs.y);
     float4 map;
-    if (__all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f))
-      map = n == kTile<T> ? make_maps<T, true, PACKED, true>(in, marks, k, n - first, p, d, a, b)
-                          : make_maps<T, false, PACKED, true>(in, marks, k, n - first, p, d, a, b);
+    if (__all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f) && begins == 0)
+      map = n == kTile<T>
+                ? make_maps<T, true, false, true>(in, marks, 0, k, n - first, p, d, a, b)
+                : make_maps<T, false, false, true>(in, marks, 0, k, n - first, p, d, a, b);
     else
-      map = make_maps<T, false, PACKED, false>(in, marks, k, n - first, p, d, a, b);
+      map = make_maps<T, false, PACKED, false>(in, marks, begins, k, n - first, p, d, a, b);
     sm.seg[half][warp][lane] = map;
-    int ends = 0;  // packed rows: which of the thread's tokens end a sequence
-    if (PACKED && p.h_out != nullptr) {
-#pragma unroll
-      for (int i = 0; i < kTokens<T>; ++i)
-        if (i < n - first && (marks[i] & kLast)) ends |= 1 << i;
-    }
     typename Pair<T>::V gate[GATED ? kTokens<T> : 1];
     if (GATED) {
 #pragma unroll
@@ -345,15 +363,29 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.segs[half]);
     const int64_t token = (int64_t)q.row * p.L + t0 + first;
-    if (!mbar_wait_bounded(&sm.segs[half], phase, &g_gs_errors)) return;
+    segments_done();
     // the segments before this one as one map
     float4 pre = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-    for (int k = 0; k < warp; ++k) pre = gs_then(pre, sm.seg[half][k][lane]);
+    if (PACKED) {
+      for (int k = 0; k < warp; ++k) pre = gs_then(pre, sm.seg[half][k][lane]);
+    } else {
+      F2 A = f2(1.0f), H = f2(0.0f);
+#pragma unroll
+      for (int k = 0; k < kWarps - 1; ++k)
+        if (k < warp) {
+          const float4 m = sm.seg[half][k][lane];
+          A = mul2(A, f2(m.x, m.y));
+          H = fma2(f2(m.x, m.y), H, f2(m.z, m.w));
+        }
+      const float2 x = unpack(A), y = unpack(H);
+      pre = make_float4(x.x, x.y, y.x, y.y);
+    }
     const int tile = (q.step * p.rows + q.row) * p.nblk + q.cb;
     const bool tells = warp == kWarps - 1 && q.step < p.steps - 1;
     if (tells) map = gs_then(pre, map);  // of the tile
     if (tells && q.step > 0) record_put(p.maps + (int64_t)tile * 32 + lane, map);
-    if (!mbar_wait_bounded(&sm.entered[half], phase, &g_gs_errors)) return;
+    entered_wait(half);
+    if (*reinterpret_cast<volatile int *>(&sm.dead)) return;
     const float2 enter = sm.enter[half][lane];
     if (tells) {
       const float2 leave = gs_through(map, enter);
@@ -364,27 +396,32 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
     }
     const float2 h = gs_through(pre, enter);
     F2 hh = f2(h.x, h.y);
-    T *y = static_cast<T *>(p.y) + token * p.D + d;
+    if (p.y != nullptr) {
+      T *y = static_cast<T *>(p.y) + token * p.D + d;
+      auto run = [&](auto all) {  // all: every token of every lane is stored, no sequence's end
 #pragma unroll
-    for (int i = 0; i < kTokens<T>; ++i) {
-      if (PACKED) {
-        const float2 ai = unpack(a[i]), bi = unpack(b[i]), hi = unpack(hh);
-        const float2 e = gs_through(make_float4(ai.x, ai.y, bi.x, bi.y), hi);
-        hh = f2(e.x, e.y);
-      } else {
-        hh = fma2(a[i], hh, b[i]);
-      }
-      if (p.y != nullptr && real && i < n - first) {
-        F2 o = hh;
-        if (GATED) {
-          const float2 z = Pair<T>::get(gate[i]);
-          o = mul2(hh, mul2(f2(z.x, z.y), sigmoid2(f2(z.x, z.y))));
+        for (int i = 0; i < kTokens<T>; ++i) {
+          if (!decltype(all)::value && PACKED && (begins >> i & 1)) hh = b[i];
+          else hh = fma2(a[i], hh, b[i]);
+          F2 o = hh;
+          if (GATED) {
+            const float2 z = Pair<T>::get(gate[i]);
+            o = mul2(hh, mul2(f2(z.x, z.y), sigmoid2(f2(z.x, z.y))));
+          }
+          if (decltype(all)::value) {
+            store_pair(y, unpack(o));
+          } else if (real && i < n - first) {
+            store_pair(y, unpack(o));
+            if (PACKED && (ends >> i & 1))
+              *reinterpret_cast<float2 *>(
+                  p.h_out + (int64_t)(p.marks[t0 + first + i] >> 2) * p.D + d) = unpack(hh);
+          }
+          y += p.D;
         }
-        store_pair(y + (int64_t)i * p.D, unpack(o));
-        if (PACKED && (ends >> i & 1))
-          *reinterpret_cast<float2 *>(p.h_out + (int64_t)(p.marks[t0 + first + i] >> 2) * p.D +
-                                      d) = unpack(hh);
-      }
+      };
+      if (__all_sync(0xffffffffu, real && n - first >= kTokens<T> && (begins | ends) == 0))
+        run(std::true_type());
+      else run(std::false_type());
     }
     if (!PACKED && p.h_out != nullptr && q.step == p.steps - 1 && real && first < n &&
         n <= first + kTokens<T>)

@@ -282,10 +282,12 @@ __device__ __forceinline__ float2 record_get(const float2 *p) {
   asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ bool is_set(float v) { return __float_as_uint(v) != kUnset; }
-__device__ __forceinline__ bool is_set(float2 v) { return is_set(v.x) && is_set(v.y); }
+__device__ __forceinline__ bool is_set(float2 v) {
+  return max(__float_as_uint(v.x), __float_as_uint(v.y)) != kUnset;
+}
 __device__ __forceinline__ bool is_set(float4 v) {
-  return is_set(v.x) && is_set(v.y) && is_set(v.z) && is_set(v.w);
+  return max(max(__float_as_uint(v.x), __float_as_uint(v.y)),
+             max(__float_as_uint(v.z), __float_as_uint(v.w))) != kUnset;
 }
 // Whether a phase is complete, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
@@ -297,6 +299,30 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
+}
+
+// Waits for a phase, for at most kWaitLimitNs; false (and the flag) if it never came.  The
+// hint lets the hardware park the warp instead of having it ask again and again, which
+// took a third of all instructions issued.
+__device__ __forceinline__ bool mbar_wait_parked(uint64_t *bar, uint32_t parity,
+                                                 unsigned int *err) {
+  unsigned long long since = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return true;
+    const unsigned long long now = globaltimer_ns();
+    if (since == 0) since = now;
+    if (now - since > kWaitLimitNs) {
+      atomicOr(err, kErrWaitTimeout);
+      return false;
+    }
+  }
 }
 
 // The map of a state across a stretch of tokens, h_out = A h_in + H, for two channels:
