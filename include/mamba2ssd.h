@@ -370,7 +370,7 @@ MAMBA2_API int mamba2_conv_ssd_prefill_backward(
  * fp32 and owned by the caller, as the SSM state is. */
 
 /* Tokens of a checkpoint (see mamba2_gated_scan_prefill). */
-#define MAMBA2_GATED_SCAN_CHUNK 128
+#define MAMBA2_GATED_SCAN_CHUNK 16
 
 typedef struct {
   int64_t batch;     /* b >= 0: sequences */
@@ -386,7 +386,7 @@ MAMBA2_API size_t mamba2_gated_scan_workspace_size(const mamba2_gated_scan_dims 
 MAMBA2_API size_t mamba2_gated_scan_backward_workspace_size(const mamba2_gated_scan_dims *dims,
                                                             int packed);
 
-/* fp32 values of the checkpoints of a prefill: rows * ceil(L / 128) * D, rows =
+/* fp32 values of the checkpoints of a prefill: rows * ceil(L / 16) * D, rows =
  * batch, or 1 for packed rows (0 if the dims are invalid). */
 MAMBA2_API size_t mamba2_gated_scan_checkpoint_count(const mamba2_gated_scan_dims *dims,
                                                      int packed);
@@ -409,8 +409,8 @@ MAMBA2_API size_t mamba2_gated_scan_checkpoint_count(const mamba2_gated_scan_dim
  *          the state entering the first token (else it is zero); on return the
  *          state after the last.  A sequence without tokens keeps its state (or
  *          gets zero).
- *  checkpoints  NULL, or fp32 [rows, ceil(L / 128), D], 16-byte aligned: receives
- *          the state entering tokens 0, 128, 256, ... of each row, for the
+ *  checkpoints  NULL, or fp32 [rows, ceil(L / 16), D], 16-byte aligned: receives
+ *          the state entering tokens 0, 16, 32, ... of each row, for the
  *          backward pass.  (In packed rows it is the state left by the token
  *          before, whatever its sequence; token 0's is zero.)
  *  workspace  >= mamba2_gated_scan_workspace_size bytes, 256-byte aligned;

@@ -441,7 +441,7 @@ def prefill_backward(dims, params, xBC, z, dt_raw, dy, conv_state_in=None, ssm_s
 # ---------------------------------------------------------------- gated scan
 
 #: Tokens of a checkpoint of the gated scan.
-GATED_SCAN_CHUNK = 128
+GATED_SCAN_CHUNK = 16
 
 
 def make_gated_scan_dims(batch, seqlen, width, *, io_dtype="bf16",
@@ -462,7 +462,7 @@ def mamba2_gated_scan_backward_workspace_size(dims: Mamba2GatedScanDims,
 
 
 def gated_scan_checkpoints(dims: Mamba2GatedScanDims, packed: bool = False, device="cuda"):
-    """An fp32 tensor for the checkpoints of one prefill: [rows, ceil(L / 128), D]."""
+    """An fp32 tensor for the checkpoints of one prefill: [rows, ceil(L / 16), D]."""
     import torch
     rows = (1 if dims.seqlen > 0 else 0) if packed else dims.batch
     return torch.empty(rows, -(-dims.seqlen // GATED_SCAN_CHUNK), dims.width,

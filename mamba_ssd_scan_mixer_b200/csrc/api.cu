@@ -160,6 +160,8 @@ MAMBA2_API int mamba2_device_errors(unsigned int *flags) {
   *flags |= f;
   if (take_gated_scan_errors(&f) != cudaSuccess) return MAMBA2_ERR_CUDA;
   *flags |= f;
+  if (take_gated_scan_backward_errors(&f) != cudaSuccess) return MAMBA2_ERR_CUDA;
+  *flags |= f;
   if (take_state_cache_errors(&f) != cudaSuccess) return MAMBA2_ERR_CUDA;
   *flags |= f;
   return MAMBA2_OK;
@@ -170,7 +172,8 @@ MAMBA2_API int mamba2_debug_stall_waits(int enable) {
   if (cudaDeviceSynchronize() != cudaSuccess) return MAMBA2_ERR_CUDA;
   if (set_step_stall((unsigned)enable) != cudaSuccess ||
       set_prefill_tc_stall((unsigned)enable) != cudaSuccess ||
-      set_gated_scan_stall((unsigned)enable) != cudaSuccess)
+      set_gated_scan_stall((unsigned)enable) != cudaSuccess ||
+      set_gated_scan_backward_stall((unsigned)enable) != cudaSuccess)
     return MAMBA2_ERR_CUDA;
   return MAMBA2_OK;
 }

@@ -14,7 +14,7 @@
 
 namespace m2 {
 
-// Tokens of one tile of the scan, and of one checkpoint.
+// Tokens of one checkpoint.
 constexpr int kGsChunk = MAMBA2_GATED_SCAN_CHUNK;
 
 struct GatedScanArgs {
@@ -53,13 +53,11 @@ cudaError_t gated_scan_backward(const GatedScanBackwardArgs &a);
 size_t gated_scan_backward_workspace(int64_t rows, int64_t L, int D, int io, bool packed);
 cudaError_t take_gated_scan_errors(unsigned int *out);
 cudaError_t set_gated_scan_stall(unsigned int v);
-// Sets *bad to whether the offsets of packed rows are wrong (and raises the flag).
-void gated_scan_check(const int32_t *cu, int64_t batch, int64_t L, unsigned int *bad,
-                      cudaStream_t stream);
-
-// Tiles of 64 tokens and 64 channels in a call: they are counted in 32 bits.
+cudaError_t take_gated_scan_backward_errors(unsigned int *out);
+cudaError_t set_gated_scan_backward_stall(unsigned int v);
+// Tiles of 32 tokens and 64 channels in a call: they are counted in 32 bits.
 inline int64_t gs_tiles(int64_t rows, int64_t L, int64_t D) {
-  return rows * ceil_div(L, 64) * ceil_div(D, 64);
+  return rows * ceil_div(L, 32) * ceil_div(D, 64);
 }
 
 // ---------------------------------------------------------------- arithmetic
@@ -251,10 +249,10 @@ struct ContextOnce {
   }
 };
 
-// [rows][L][D] with a token stride of ld elements, in boxes of one tile; false if it
-// cannot be described.
+// [rows][L][D] with a token stride of ld elements, in boxes of `tokens` by 64 channels;
+// false if it cannot be described.
 bool gs_tensor_map(CUtensorMap *m, int io, const void *base, int64_t rows, int64_t L, int D,
-                   int64_t ld);
+                   int64_t ld, int tokens);
 
 // Records that blocks pass to one another.  A word that has not been written holds
 // kUnset, a NaN that no arithmetic gives, so that each word tells by itself whether it is
@@ -357,6 +355,9 @@ template <> struct Pair<__nv_bfloat16> {
 };
 template <typename T> __device__ __forceinline__ float2 ld2(const T *p) {
   return Pair<T>::get(*reinterpret_cast<const typename Pair<T>::V *>(p));
+}
+template <typename T> __device__ __forceinline__ void st2(T *p, float2 v) {
+  *reinterpret_cast<typename Pair<T>::V *>(p) = Pair<T>::put(v.x, v.y);
 }
 template <typename T> __device__ __forceinline__ void st2(T *p, float a, float b) {
   *reinterpret_cast<typename Pair<T>::V *>(p) = Pair<T>::put(a, b);

@@ -1,277 +1,494 @@
 // Backward pass of the gated linear recurrence (gated_scan.cuh).
 //
-// With d_t the gradient of h_t (of the last token's: plus the final state's),
+// With d_t the gradient of h_t (of a sequence's last: plus the final state's), and
+// v = 1 - a^2,
 //     d_t  = dy_t silu(z_t) + a_{t+1} d_{t+1}
-//     dx   = d m G               dg = d m x G (1 - G)        dz = dy h silu'(z)
-//     dla  = d (a h_{t-1} - a^2 / m G x)
+//     dx   = d m G               dg = dx x (1 - G)           dz = dy h silu'(z)
+//     dla  = d a (h_{t-1} - a b / v)                         (b = m G x; a^2 / m G x = a^2 b / v)
 //     dr   = dla la (1 - R)      dlam = sum dla (-c R) sigmoid(lam)
-#include "gated_scan.cuh"
+//
+// What a token hands to the one before it, E_t = a_t d_t = a_t E_{t+1} + a_t dy_t silu(z_t),
+// is the prefill's recurrence run from the last token to the first.  So:
+//   1. gs_back_carry_kernel, built like the prefill's, runs it over r, dy and z, and
+//      writes E only where 16 tokens end;
+//   2. gs_back_apply_kernel then has, for each 16 tokens, the state that enters them (the
+//      prefill's checkpoints) and the E that does: its warps depend on nobody.  Each runs
+//      its 16 tokens forwards, keeping h, R and G in registers, and backwards.
+// The first pass costs 4 bytes an element beside the second's 14 (bf16), but the second
+// begins where the first ended, with the tokens whose r and dy are still in L2.  One pass
+// over everything would have to keep a tile's coefficients while the E entering it is
+// looked up, which halves the tiles under way.
+#include "gated_scan_tiles.cuh"
 
 namespace m2 {
 namespace {
 
-constexpr int kThreads = 64;  // two channels each
-constexpr int kSub = 16;      // tokens whose states are held in registers
+static_assert(kGsChunk == 16, "tokens of a thread, between checkpoints");
 
-template <typename T> struct Bwd {
-  const T *x, *r, *g, *z, *dy;
-  int64_t ld_x, ld_r, ld_g, ld_z;
-  const float *lam, *h_in, *dh, *ck;
+// ---------------------------------------------------------------- E at the chunks' ends
+template <typename T, bool GATED> using CarryTiles = Shared<T, GATED ? 3 : 2, 64>;
+template <typename T, bool GATED>
+constexpr int kCarryResident = sizeof(T) == 2 ? (GATED ? 4 : 5) : (GATED ? 2 : 3);
+
+__device__ __forceinline__ F2 silu2(F2 z) { return mul2(z, sigmoid2(z)); }
+
+// The map of a thread's 16 tokens, last to first.  `lasts`: the tokens that end a sequence.
+template <typename S, bool FULL, bool RESETS, bool NEAR, bool GATED>
+__device__ __forceinline__ float4 back_map(const unsigned char *in, const int *marks,
+                                           unsigned int lasts, F2 ncs, int n, const float *dh,
+                                           int D, int d) {
+  using T = typename S::T;
+  F2 A = f2(1.0f), E = f2(0.0f);
+#pragma unroll
+  for (int i = S::kTokens - 1; i >= 0; --i) {
+    if (!FULL && i >= n) continue;
+    const unsigned char *row = in + i * S::kRow;
+    F2 a, less, dy = gs_pair<T>(row + S::kTensor);
+    decay2<NEAR>(mul2(ncs, sigmoid2(gs_pair<T>(row))), &a, &less);
+    if (GATED) dy = mul2(dy, silu2(gs_pair<T>(row + 2 * S::kTensor)));
+    if (RESETS && (lasts >> i & 1)) {
+      if (dh != nullptr && d < D) {
+        const float2 v = *reinterpret_cast<const float2 *>(dh + (int64_t)(marks[i] >> 2) * D + d);
+        dy = add2(dy, f2(v.x, v.y));
+      }
+      A = f2(-0.0f);
+      E = mul2(a, dy);
+    } else {
+      A = mul2(A, a);
+      E = mul2(a, add2(E, dy));
+    }
+  }
+  const float2 x = unpack(A), y = unpack(E);
+  return make_float4(x.x, x.y, y.x, y.y);
+}
+
+template <typename T, bool PACKED, bool GATED>
+__global__ void __launch_bounds__(kThreads, (kCarryResident<T, GATED>))
+    gs_back_carry_kernel(const __grid_constant__ Maps maps, const Scan p, const float *dh,
+                         float *carry) {
+  using S = CarryTiles<T, GATED>;
+  extern __shared__ __align__(128) unsigned char raw[];
+  S &sm = *reinterpret_cast<S *>(raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (!begin<S, PACKED>(sm, p)) return;
+  launch_dependents();
+  if (warp == kWarps) {
+    look_up<S, PACKED, true>(sm, maps, p);
+    return;
+  }
+  const int first = (kWarps - 1 - warp) * S::kTokens;  // of the warp's tokens
+  const int64_t nch = (p.L + kGsChunk - 1) / kGsChunk;
+  for (int it = 0;; ++it) {
+    const int s = it % S::kStages, half = it & 1;
+    if (!mbar_wait_parked(&sm.full[s], (it / S::kStages) & 1, &g_gs_errors)) sm.dead = 1;
+    const Tile q = sm.tile[s];
+    if (q.left <= 0) return;
+    const int t0 = (p.steps - 1 - q.step) * S::kTile, n = (int)min((int64_t)S::kTile, p.L - t0);
+    const int d = q.cb * kWidth + 2 * lane;
+    const float2 ncs = *reinterpret_cast<const float2 *>(&sm.ncs[s][2 * lane]);
+    const F2 k = f2(ncs.x, ncs.y);
+    const unsigned char *in = sm.in[s] + first * S::kRow + lane * (2 * (int)sizeof(T));
+    const int *marks = sm.marks[s] + first;
+    unsigned int lasts = 0;
+    if (PACKED)
+      lasts = __ballot_sync(0xffffffffu, lane < min(S::kTokens, n - first) && (marks[lane] & kLast));
+    float4 map;
+    if (__all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f) && lasts == 0 && n == S::kTile)
+      map = back_map<S, true, false, true, GATED>(in, marks, 0, k, n - first, dh, p.D, d);
+    else
+      map = back_map<S, false, PACKED, false, GATED>(in, marks, lasts, k, n - first, dh, p.D, d);
+    sm.seg[half][warp][lane] = map;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.segs[half]);
+    float2 e;
+    if (!exchange<PACKED>(sm, p, q, half, warp, lane, map, &e)) return;
+    if (d < p.D && first < n)
+      *reinterpret_cast<float2 *>(
+          carry + ((int64_t)q.row * nch + (t0 + first) / kGsChunk) * p.D + d) = e;
+  }
+}
+
+// ---------------------------------------------------------------- the gradients
+constexpr int kApplyTile = 64;
+
+template <typename T, bool GATED> struct ApplyShared {
+  static constexpr int kTensors = GATED ? 5 : 4;
+  // one stage where two would leave too few blocks to an SM
+  static constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
+  static constexpr int kRow = kWidth * (int)sizeof(T), kTensor = kApplyTile * kRow;
+  alignas(128) unsigned char in[kStages][kTensors * kTensor];
+  alignas(16) float h[kStages][kWarps][kWidth];  // the states entering the warps' tokens
+  alignas(16) float e[kStages][kWarps][kWidth];  // and the E
+  alignas(16) int marks[kStages][kApplyTile];
+  alignas(16) float ncs[kStages][kWidth];
+  float2 dl[2][kWarps][32];
+  uint64_t full[kStages];
+  int dead;  // a wait ran out: everybody leaves after the tile
+};
+// Three blocks of four warps: 168 registers a thread.
+constexpr int kApplyThreads = 32 * kWarps;
+template <typename T, bool GATED>
+constexpr int kApplyResident = GATED ? 2 : 3;
+
+template <typename T> struct Apply {
+  Scan p;
+  const float *ck, *carry;  // [rows][chunks][D]
+  const float *h_in, *dh;   // packed rows: the sequences' initial states and final gradients
   T *dx, *dr, *dg, *dz;
-  float *dh_in;
-  float c;
-  int64_t L, nch, batch;
-  int D;
-  const int32_t *cu;
-  float *P, *Q, *carry, *dlam_part;
-  const unsigned int *bad;
+  float *dh_in, *dl;  // dl: [rows * steps][nblk * 64]
+  unsigned long long zero;
 };
 
-__device__ __forceinline__ float2 silu2(float2 z) {
-  return make_float2(z.x * gs_sigmoid(z.x), z.y * gs_sigmoid(z.y));
-}
-
-// What a chunk hands to the token before it (a d of its first token), as a map
-// of what it is handed: out = P in + Q.
-template <typename T> __global__ void gs_back_chunk_kernel(Bwd<T> p) {
-  __shared__ int first[kGsChunk], last[kGsChunk];
-  if (p.cu != nullptr && *p.bad) return;
-  const int64_t rc = blockIdx.x, row = rc / p.nch, t0 = (rc % p.nch) * kGsChunk;
-  const int n = (int)min((int64_t)kGsChunk, p.L - t0);
-  if (p.cu != nullptr) gs_marks(p.cu, p.batch, t0, n, first, last);
-  const int d = 2 * (blockIdx.y * kThreads + threadIdx.x);
-  if (d >= p.D) return;
-  const float ncs0 = -p.c * softplus_f(p.lam[d]), ncs1 = -p.c * softplus_f(p.lam[d + 1]);
-  float2 P = make_float2(1.0f, 1.0f), e = make_float2(0.0f, 0.0f);
-  for (int i = n - 1; i >= 0; --i) {
-    const int64_t t = row * p.L + t0 + i;
-    const float2 r = ld2(p.r + t * p.ld_r + d);
-    float2 dy = ld2(p.dy + t * p.D + d);
-    if (p.z != nullptr) {
-      const float2 s = silu2(ld2(p.z + t * p.ld_z + d));
-      dy.x *= s.x;
-      dy.y *= s.y;
-    }
-    if (p.cu != nullptr && last[i] >= 0 && p.dh != nullptr) {
-      const float2 f = *reinterpret_cast<const float2 *>(p.dh + (int64_t)last[i] * p.D + d);
-      dy.x += f.x;
-      dy.y += f.y;
-    }
-    const float a0 = expf(ncs0 * gs_sigmoid(r.x)), a1 = expf(ncs1 * gs_sigmoid(r.y));
-    e.x = a0 * (dy.x + e.x);
-    e.y = a1 * (dy.y + e.y);
-    P.x *= a0;
-    P.y *= a1;
-    if (p.cu != nullptr && first[i] >= 0) P = e = make_float2(0.0f, 0.0f);
-  }
-  *reinterpret_cast<float2 *>(p.P + rc * p.D + d) = P;
-  *reinterpret_cast<float2 *>(p.Q + rc * p.D + d) = e;
-}
-
-template <typename T> __global__ void gs_back_carry_kernel(Bwd<T> p) {
-  if (p.cu != nullptr && *p.bad) return;
-  const int d = blockIdx.x * blockDim.x + threadIdx.x;
-  if (d >= p.D) return;
-  const int64_t row = blockIdx.y;
-  float e = p.cu == nullptr && p.dh != nullptr ? p.dh[row * p.D + d] : 0.0f;
-  for (int64_t j = p.nch - 1; j >= 0; --j) {
-    const int64_t o = (row * p.nch + j) * p.D + d;
-    p.carry[o] = e;
-    e = p.P[o] == 0.0f ? p.Q[o] : p.P[o] * e + p.Q[o];
-  }
-  if (p.cu == nullptr && p.dh_in != nullptr) p.dh_in[row * p.D + d] = e;
-}
-
-template <typename T> __global__ void gs_back_apply_kernel(Bwd<T> p) {
-  __shared__ int first[kGsChunk], last[kGsChunk];
-  if (p.cu != nullptr && *p.bad) return;
-  const int64_t rc = blockIdx.x, row = rc / p.nch, t0 = (rc % p.nch) * kGsChunk;
-  const int n = (int)min((int64_t)kGsChunk, p.L - t0);
-  if (p.cu != nullptr) gs_marks(p.cu, p.batch, t0, n, first, last);
-  const int d = 2 * (blockIdx.y * kThreads + threadIdx.x);
-  if (d >= p.D) return;
-  const float ncs[2] = {-p.c * softplus_f(p.lam[d]), -p.c * softplus_f(p.lam[d + 1])};
-  const float2 c0 = *reinterpret_cast<const float2 *>(p.ck + rc * p.D + d);
-  const float2 e0 = *reinterpret_cast<const float2 *>(p.carry + rc * p.D + d);
-  float start[kGsChunk / kSub][2], h[2] = {c0.x, c0.y}, e[2] = {e0.x, e0.y};
-  float dl[2] = {0.0f, 0.0f};
-  auto state_before = [&](int i) {  // a sequence's first token starts from its own state
-    if (p.cu == nullptr || first[i] < 0) return;
-    const float2 v = p.h_in != nullptr ? *reinterpret_cast<const float2 *>(
-                                             p.h_in + (int64_t)first[i] * p.D + d)
-                                       : make_float2(0.0f, 0.0f);
-    h[0] = v.x;
-    h[1] = v.y;
-  };
-  for (int i = 0; i < n; ++i) {
-    const int64_t t = row * p.L + t0 + i;
-    if (i % kSub == 0) {
-      start[i / kSub][0] = h[0];
-      start[i / kSub][1] = h[1];
-    }
-    state_before(i);
-    const float2 x = ld2(p.x + t * p.ld_x + d), r = ld2(p.r + t * p.ld_r + d),
-                 g = ld2(p.g + t * p.ld_g + d);
-    const Gate u = gs_gate(r.x, g.x, ncs[0]), v = gs_gate(r.y, g.y, ncs[1]);
-    h[0] = u.a * h[0] + u.m * u.G * x.x;
-    h[1] = v.a * h[1] + v.m * v.G * x.y;
-  }
-  for (int b = (n - 1) / kSub; b >= 0; --b) {
-    float before[kSub][2];
-    const int i1 = min(n, (b + 1) * kSub);
-    h[0] = start[b][0];
-    h[1] = start[b][1];
-    for (int i = b * kSub; i < i1; ++i) {
-      const int64_t t = row * p.L + t0 + i;
-      state_before(i);
-      before[i - b * kSub][0] = h[0];
-      before[i - b * kSub][1] = h[1];
-      const float2 x = ld2(p.x + t * p.ld_x + d), r = ld2(p.r + t * p.ld_r + d),
-                   g = ld2(p.g + t * p.ld_g + d);
-      const Gate u = gs_gate(r.x, g.x, ncs[0]), v = gs_gate(r.y, g.y, ncs[1]);
-      h[0] = u.a * h[0] + u.m * u.G * x.x;
-      h[1] = v.a * h[1] + v.m * v.G * x.y;
-    }
-    for (int i = i1 - 1; i >= b * kSub; --i) {
-      const int64_t t = row * p.L + t0 + i;
-      const float2 x2 = ld2(p.x + t * p.ld_x + d), r2 = ld2(p.r + t * p.ld_r + d),
-                   g2 = ld2(p.g + t * p.ld_g + d), dy2 = ld2(p.dy + t * p.D + d);
-      const float x[2] = {x2.x, x2.y}, r[2] = {r2.x, r2.y}, g[2] = {g2.x, g2.y},
-                  dy[2] = {dy2.x, dy2.y};
-      float z[2] = {0.0f, 0.0f}, dx[2], dr[2], dg[2], dz[2];
-      if (p.z != nullptr) {
-        const float2 z2 = ld2(p.z + t * p.ld_z + d);
-        z[0] = z2.x;
-        z[1] = z2.y;
-      }
+// One warp's 16 tokens.  FAST: all of them there, no sequence begins or ends among them,
+// and decays near one.
+template <typename T, bool GATED, bool PACKED, bool FAST>
+__device__ __forceinline__ F2 apply_tokens(const ApplyShared<T, GATED> &sm, int s,
+                                           const Apply<T> &q, int row, int64_t t0, int n, int first,
+                                           int lane, int d) {
+  using S = ApplyShared<T, GATED>;
+  constexpr int K = kGsChunk, kTensor = S::kTensor;
+  const Scan &p = q.p;
+  const int warp = first / K;
+  const unsigned char *in = sm.in[s] + first * S::kRow + lane * (2 * (int)sizeof(T));
+  const int *marks = sm.marks[s] + first;
+  const float2 nn = *reinterpret_cast<const float2 *>(&sm.ncs[s][2 * lane]);
+  const F2 ncs = f2(nn.x, nn.y);
+  const float2 h0 = *reinterpret_cast<const float2 *>(&sm.h[s][warp][2 * lane]);
+  const float2 e0 = *reinterpret_cast<const float2 *>(&sm.e[s][warp][2 * lane]);
+  F2 h = f2(h0.x, h0.y), e = f2(e0.x, e0.y), dl = f2(0.0f);
+  const bool real = d < p.D;
+  const int count = FAST ? K : min(K, n - first);
+  F2 R[K], G[K], before[K];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const Gate q = gs_gate(r[k], g[k], ncs[k]);
-        const float hp = before[i - b * kSub][k], ht = q.a * hp + q.m * q.G * x[k];
-        float dh = dy[k];
-        if (p.z != nullptr) {
-          const float s = gs_sigmoid(z[k]);
-          dz[k] = dy[k] * ht * s * (1.0f + z[k] * (1.0f - s));
-          dh *= z[k] * s;
-        }
-        if (p.cu != nullptr && last[i] >= 0 && p.dh != nullptr)
-          dh += p.dh[(int64_t)last[i] * p.D + d + k];
-        const float dt = dh + e[k];
-        dx[k] = dt * q.m * q.G;
-        dg[k] = dx[k] * x[k] * (1.0f - q.G);
-        // as la -> 0 both la / m and R / m go to zero with m
-        const float per_m = q.m > 0.0f ? 1.0f / q.m : 0.0f;
-        const float dla = dt * (q.a * hp - q.a * q.a * per_m * q.G * x[k]);
-        dr[k] = dla * q.la * (1.0f - q.R);
-        dl[k] += dla * q.R;
-        e[k] = q.a * dt;
-      }
-      st2(p.dx + t * p.D + d, dx[0], dx[1]);
-      st2(p.dr + t * p.D + d, dr[0], dr[1]);
-      st2(p.dg + t * p.D + d, dg[0], dg[1]);
-      if (p.z != nullptr) st2(p.dz + t * p.D + d, dz[0], dz[1]);
-      if (p.cu != nullptr && first[i] >= 0) {
-        if (p.dh_in != nullptr)
-          *reinterpret_cast<float2 *>(p.dh_in + (int64_t)first[i] * p.D + d) =
-              make_float2(e[0], e[1]);
-        e[0] = e[1] = 0.0f;
+  for (int i = 0; i < K; ++i) {
+    if (!FAST && i >= count) continue;
+    if (!FAST && PACKED && (marks[i] & kFirst)) {
+      h = f2(0.0f);
+      if (q.h_in != nullptr && real) {
+        const float2 v = *reinterpret_cast<const float2 *>(q.h_in + (int64_t)(marks[i] >> 2) * p.D + d);
+        h = f2(v.x, v.y);
       }
     }
+    const unsigned char *at = in + i * S::kRow;
+    const Coeffs c = coefficients<FAST>(gs_pair<T>(at), gs_clamped<T>(at + kTensor),
+                                        gs_clamped<T>(at + 2 * kTensor), ncs);
+    R[i] = c.R;
+    G[i] = c.G;
+    before[i] = h;
+    h = fma2(c.a, h, c.b);
   }
-  *reinterpret_cast<float2 *>(p.dlam_part + rc * p.D + d) = make_float2(dl[0], dl[1]);
+  // R, G and h alone are kept: the rest is cheaper made again than held.  (The compiler
+  // would hold it, in local memory; it does not know that `zero` is zero.)
+  const F2 ncs2 = F2{ncs.v ^ q.zero};
+  in += q.zero;
+  const int64_t out0 = ((int64_t)row * p.L + t0 + first) * p.D + d;
+#pragma unroll
+  for (int i = K - 1; i >= 0; --i) {
+    if (!FAST && i >= count) continue;
+    const unsigned char *at = in + i * S::kRow;
+    const F2 x = gs_pair<T>(at);
+    F2 dy = gs_pair<T>(at + 3 * kTensor), a, less;
+    const F2 t = mul2(ncs2, R[i]);
+    decay2<FAST>(t, &a, &less);
+    constexpr float down = 1.0f / kGateScale, down2 = down * down;
+    const F2 more = fma2(a, f2(-1.0f), f2(-1.0f));
+    const float2 v = unpack(mul2(less, more)), w = unpack(mul2(less, mul2(more, f2(down2))));
+    const float m0 = sqrt_ap(w.x), m1 = sqrt_ap(w.y);
+    const F2 mG = mul2(f2(m0, m1), G[i]);
+    const F2 b = mul2(mG, x);
+    if (GATED) {
+      const F2 z = gs_pair<T>(at + 4 * kTensor), sig = sigmoid2(z);
+      const F2 ht = fma2(a, before[i], b);
+      // silu' = sig (1 + z (1 - sig))
+      const F2 slope = mul2(sig, fma2(z, fma2(sig, f2(-1.0f), f2(1.0f)), f2(1.0f)));
+      if (real) st2(q.dz + out0 + (int64_t)i * p.D, unpack(mul2(mul2(dy, ht), slope)));
+      dy = mul2(dy, mul2(z, sig));
+    }
+    if (!FAST && PACKED && (marks[i] & kLast)) {
+      e = f2(0.0f);
+      if (q.dh != nullptr && real) {
+        const float2 g = *reinterpret_cast<const float2 *>(q.dh + (int64_t)(marks[i] >> 2) * p.D + d);
+        e = f2(g.x, g.y);
+      }
+    }
+    const F2 dd = add2(dy, e);
+    const F2 dx = mul2(dd, mG);
+    const F2 dg = mul2(mul2(dx, x), fma2(G[i], f2(-down), f2(1.0f)));
+    // where v is next to nothing m, and b with it, was taken for zero: so is b / v
+    const F2 iv = f2(rcp(max_nan(v.x, 1.3e-17f)), rcp(max_nan(v.y, 1.3e-17f)));
+    e = mul2(a, dd);
+    const F2 dla = mul2(e, fma2(mul2(a, b), mul2(iv, f2(-1.0f)), before[i]));
+    dl = fma2(dla, R[i], dl);
+    const F2 dr = mul2(mul2(dla, mul2(t, f2(0.6931471805599453f))), fma2(R[i], f2(-1.0f), f2(1.0f)));
+    if (real) {
+      const int64_t o = out0 + (int64_t)i * p.D;
+      st2(q.dx + o, unpack(dx));
+      // a gate so shut that m counts as zero (r = -inf) gets no gradient
+      const float2 g = unpack(dr);
+      st2(q.dr + o, m0 == 0.0f ? 0.0f : g.x, m1 == 0.0f ? 0.0f : g.y);
+      st2(q.dg + o, unpack(dg));
+    }
+    if (!FAST && PACKED && (marks[i] & kFirst) && q.dh_in != nullptr && real)
+      *reinterpret_cast<float2 *>(q.dh_in + (int64_t)(marks[i] >> 2) * p.D + d) = unpack(e);
+  }
+  if (!PACKED && t0 + first == 0 && q.dh_in != nullptr && real)
+    *reinterpret_cast<float2 *>(q.dh_in + (int64_t)row * p.D + d) = unpack(e);
+  return dl;
 }
 
-// Packed rows: a sequence without tokens hands its state's gradient on.
-__global__ void gs_back_empty_kernel(const int32_t *cu, const float *dh, float *dh_in, int64_t n,
-                                     int D, const unsigned int *bad) {
-  if (*bad) return;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x)
-    if (cu[i / D + 1] <= cu[i / D]) dh_in[i] = dh != nullptr ? dh[i] : 0.0f;
+template <typename T, bool PACKED, bool GATED>
+__global__ void __launch_bounds__(kApplyThreads, (kApplyResident<T, GATED>))
+    gs_back_apply_kernel(const __grid_constant__ Maps maps, const Apply<T> q) {
+  using S = ApplyShared<T, GATED>;
+  extern __shared__ __align__(128) unsigned char raw[];
+  S &sm = *reinterpret_cast<S *>(raw);
+  const Scan &p = q.p;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (test_stall(&g_gs_stall, &g_gs_errors)) return;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) mbar_init(&sm.full[s], 1);
+    sm.dead = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  launch_dependents();
+  if (PACKED && *p.bad) return;
+  const int64_t nch = (p.L + kGsChunk - 1) / kGsChunk;
+  // one thread: a tile's copies, into stage s
+  auto fetch = [&](int s, int tile) {
+    if (tile >= p.tiles) return;
+    const int cb = tile % p.nblk, row = tile / p.nblk % p.rows;
+    const int t0 = tile / p.nblk / p.rows * kApplyTile;
+    const int n = (int)min((int64_t)kApplyTile, p.L - t0), chunks = (n + kGsChunk - 1) / kGsChunk;
+    const uint32_t wide = (uint32_t)min(kWidth, p.D - cb * kWidth) * 4;
+    const uint32_t mark_bytes = PACKED ? (n * 4 + 15) / 16 * 16 : 0;
+    mbar_arrive_expect_tx(&sm.full[s], S::kTensors * S::kTensor + 2 * chunks * wide + kWidth * 4 +
+                                           mark_bytes);
+#pragma unroll
+    for (int k = 0; k < S::kTensors; ++k)
+      tma_load_3d(sm.in[s] + k * S::kTensor, &maps.m[k], cb * kWidth, t0, row, &sm.full[s]);
+    const int64_t at = ((int64_t)row * nch + t0 / kGsChunk) * p.D + cb * kWidth;
+    for (int k = 0; k < chunks; ++k) {
+      bulk_g2s(sm.h[s][k], q.ck + at + (int64_t)k * p.D, wide, &sm.full[s]);
+      bulk_g2s(sm.e[s][k], q.carry + at + (int64_t)k * p.D, wide, &sm.full[s]);
+    }
+    bulk_g2s(sm.ncs[s], p.ncs + cb * kWidth, kWidth * 4, &sm.full[s]);
+    if (PACKED) bulk_g2s(sm.marks[s], p.marks + t0, mark_bytes, &sm.full[s]);
+  };
+  constexpr int kFetcher = 32 * kWarps - 1;
+  if (threadIdx.x == kFetcher)
+    for (int s = 0; s < S::kStages; ++s) fetch(s, blockIdx.x + s * gridDim.x);
+  const int first = warp * kGsChunk;
+  int it = 0;
+  for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, ++it) {
+    const int s = it % S::kStages, half = it & 1;
+    const bool there = mbar_wait_parked(&sm.full[s], (it / S::kStages) & 1, &g_gs_errors);
+    if (!there) sm.dead = 1;
+    const int cb = tile % p.nblk, row = tile / p.nblk % p.rows, step = tile / p.nblk / p.rows;
+    const int t0 = step * kApplyTile, n = (int)min((int64_t)kApplyTile, p.L - t0);
+    const int d = cb * kWidth + 2 * lane;
+    F2 dl = f2(0.0f);
+    if (there && first < n) {
+      const float2 nn = *reinterpret_cast<const float2 *>(&sm.ncs[s][2 * lane]);
+      bool fast = fminf(nn.x, nn.y) >= -0.5f && n - first >= kGsChunk;
+      if (PACKED) fast = fast && !(lane < kGsChunk && (sm.marks[s][first + lane % kGsChunk] & 3));
+      if (__all_sync(0xffffffffu, fast))
+        dl = apply_tokens<T, GATED, PACKED, true>(sm, s, q, row, t0, n, first, lane, d);
+      else
+        dl = apply_tokens<T, GATED, PACKED, false>(sm, s, q, row, t0, n, first, lane, d);
+    }
+    sm.dl[half][warp][lane] = unpack(dl);
+    segments_done();  // every warp is done with the stage
+    if (*reinterpret_cast<volatile int *>(&sm.dead)) {
+      // what this block has under way lands before it leaves
+      if (threadIdx.x == kFetcher)
+        for (int i = it; i < it + S::kStages && tile + (i - it) * (int)gridDim.x < p.tiles; ++i)
+          mbar_wait_parked(&sm.full[i % S::kStages], (i / S::kStages) & 1, &g_gs_errors);
+      return;
+    }
+    if (threadIdx.x == kFetcher) fetch(s, tile + S::kStages * (int)gridDim.x);
+    if (warp == 0) {  // (the next tile's sums go to the other half)
+      float2 v = sm.dl[half][0][lane];
+#pragma unroll
+      for (int k = 1; k < kWarps; ++k) {
+        v.x += sm.dl[half][k][lane].x;
+        v.y += sm.dl[half][k][lane].y;
+      }
+      *reinterpret_cast<float2 *>(
+          q.dl + ((int64_t)row * p.steps + step) * (p.nblk * kWidth) + d) = v;
+    }
+  }
 }
 
-__global__ void gs_dlam_kernel(const float *part, int64_t n, int D, const float *lam, float c,
-                               float *dlam, const unsigned int *bad) {
+// ---------------------------------------------------------------- dlam
+// Sums of up to kSumRows rows of `in` [n][width] each, in a fixed order; the last round
+// turns the sum into the gradient.
+constexpr int kSumRows = 512, kSumGroups = 16;
+__global__ void __launch_bounds__(32 * kSumGroups)
+    gs_sum_kernel(const float *in, int64_t n, int width, float *out, const float *lam, float c, int D,
+                  const unsigned int *bad) {
+  grid_dependency_wait();
+  launch_dependents();
   if (bad != nullptr && *bad) return;
-  const int d = blockIdx.x * blockDim.x + threadIdx.x;
-  if (d >= D) return;
+  __shared__ float part[kSumGroups][33];
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  const int d = blockIdx.x * 32 + lane;
+  const int64_t r0 = (int64_t)blockIdx.y * kSumRows, r1 = min(n, r0 + kSumRows);
   float s = 0.0f;
-  for (int64_t i = 0; i < n; ++i) s += part[i * D + d];
-  dlam[d] = -c * gs_sigmoid(lam[d]) * s;
+  if (d < width) {
+#pragma unroll 8
+    for (int64_t r = r0 + group; r < r1; r += kSumGroups) s += in[r * width + d];
+  }
+  part[group][lane] = s;
+  __syncthreads();
+  if (group != 0 || d >= width) return;
+  for (int k = 1; k < kSumGroups; ++k) s += part[k][lane];
+  if (lam == nullptr) out[(int64_t)blockIdx.y * width + d] = s;
+  else if (d < D) out[d] = -c * gs_sigmoid(lam[d]) * s;
+}
+
+// Where the parts of the backward pass's workspace are.
+struct BackPlan {
+  Plan scan;  // its own parts first
+  size_t carry, ck, dl, sums, forward, total;
+  int64_t partials;
+};
+BackPlan back_plan(int64_t rows, int64_t L, int D, int io, bool packed) {
+  BackPlan b;
+  b.scan = plan_of(rows, L, D, kApplyTile, packed);
+  const size_t chunks = (size_t)(rows * ceil_div(L, kGsChunk)) * D * 4;
+  const size_t width = (size_t)b.scan.nblk * kWidth * 4;
+  b.partials = rows * b.scan.steps;
+  b.carry = align_up(b.scan.total, 256);
+  b.ck = b.carry + align_up(chunks, 256);
+  b.dl = b.ck + align_up(chunks, 256);
+  b.sums = b.dl + (size_t)b.partials * width;
+  b.forward = b.sums + (b.partials > kSumRows ? 2 * (size_t)ceil_div(b.partials, kSumRows) * width : 0);
+  b.total = b.forward + gated_scan_workspace(rows, L, D, io, packed);
+  return b;
+}
+
+template <typename T, bool PACKED, bool GATED>
+cudaError_t launch(const GatedScanBackwardArgs &b, const Scan &p, const float *ck, float *carry,
+                   float *dl) {
+  const GatedScanArgs &a = b.f;
+  const int64_t rows = a.rows();
+  const void *in[5] = {a.x, a.r, a.g, b.dy, a.z};
+  const int64_t ld[5] = {a.ld_x, a.ld_r, a.ld_g, a.D, a.ld_z};
+  Maps apply = {}, back = {};
+  for (int k = 0; k < (GATED ? 5 : 4); ++k)
+    if (!gs_tensor_map(&apply.m[k], a.io, in[k], rows, a.L, a.D, ld[k], kApplyTile))
+      return cudaErrorInvalidValue;
+  back.m[0] = apply.m[1];
+  back.m[1] = apply.m[3];
+  back.m[2] = apply.m[4];
+  {
+    constexpr size_t smem = sizeof(CarryTiles<T, GATED>);
+    static_assert((kCarryResident<T, GATED>)*(smem + 1024 + 256) <= 228 * 1024, "blocks to an SM");
+    static ContextOnce once;
+    const cudaError_t e = launch_dependent(
+        gs_back_carry_kernel<T, PACKED, GATED>, once,
+        std::min(p.tiles, kCarryResident<T, GATED> * sm_count()), kThreads, smem, a.stream, back, p,
+        b.dh, carry);
+    if (e != cudaSuccess) return e;
+  }
+  constexpr size_t smem = sizeof(ApplyShared<T, GATED>);
+  static_assert((kApplyResident<T, GATED>)*(smem + 1024 + 256) <= 228 * 1024, "blocks to an SM");
+  static ContextOnce once;
+  Apply<T> q;
+  q.p = p;
+  q.ck = ck;
+  q.carry = carry;
+  q.h_in = b.h_in;
+  q.dh = b.dh;
+  q.dx = static_cast<T *>(b.dx);
+  q.dr = static_cast<T *>(b.dr);
+  q.dg = static_cast<T *>(b.dg);
+  q.dz = static_cast<T *>(b.dz);
+  q.dh_in = b.dh_in;
+  q.dl = dl;
+  q.zero = 0;
+  return launch_dependent(gs_back_apply_kernel<T, PACKED, GATED>, once,
+                          std::min(p.tiles, kApplyResident<T, GATED> * sm_count()), kApplyThreads, smem,
+                          a.stream, apply, q);
 }
 
 template <typename T> cudaError_t backward(const GatedScanBackwardArgs &b) {
   const GatedScanArgs &a = b.f;
-  const int64_t rows = a.rows(), nch = a.nchunks();
-  const size_t n = (size_t)rows * nch * a.D;
-  unsigned int *bad = reinterpret_cast<unsigned int *>(a.ws);
-  if (a.cu != nullptr) gated_scan_check(a.cu, a.batch, a.L, bad, a.stream);
-  float *P = reinterpret_cast<float *>(a.ws + 256), *Q = P + n, *carry = Q + n, *part = carry + n,
-        *own_ck = part + n;
+  const bool packed = a.cu != nullptr;
+  const BackPlan w = back_plan(a.rows(), a.L, a.D, a.io, packed);
   const float *ck = b.ck;
   if (ck == nullptr) {  // the forward again, for the states that enter the chunks
     GatedScanArgs f = a;
     f.y = nullptr;
     f.h = const_cast<float *>(b.h_in);
     f.states_in = b.h_in != nullptr;
-    f.ck = own_ck;
-    f.ws = a.ws + 256 + align_up(5 * n * 4, 256);
     f.no_state_out = true;
+    f.ck = reinterpret_cast<float *>(a.ws + w.ck);
+    f.ws = a.ws + w.forward;
     const cudaError_t e = gated_scan_prefill(f);
     if (e != cudaSuccess) return e;
-    ck = own_ck;
+    ck = f.ck;
   }
-  Bwd<T> p;
-  p.x = static_cast<const T *>(a.x);
-  p.r = static_cast<const T *>(a.r);
-  p.g = static_cast<const T *>(a.g);
-  p.z = static_cast<const T *>(a.z);
-  p.dy = static_cast<const T *>(b.dy);
-  p.ld_x = a.ld_x;
-  p.ld_r = a.ld_r;
-  p.ld_g = a.ld_g;
-  p.ld_z = a.ld_z;
-  p.lam = a.lam;
-  p.h_in = b.h_in;
-  p.dh = b.dh;
-  p.ck = ck;
-  p.dx = static_cast<T *>(b.dx);
-  p.dr = static_cast<T *>(b.dr);
-  p.dg = static_cast<T *>(b.dg);
-  p.dz = static_cast<T *>(b.dz);
-  p.dh_in = b.dh_in;
-  p.c = a.c;
-  p.L = a.L;
-  p.nch = nch;
-  p.batch = a.batch;
-  p.D = a.D;
-  p.cu = a.cu;
-  p.P = P;
-  p.Q = Q;
-  p.carry = carry;
-  p.dlam_part = part;
-  p.bad = bad;
-  const dim3 grid((unsigned)(rows * nch), (unsigned)ceil_div(a.D / 2, kThreads));
-  gs_back_chunk_kernel<T><<<grid, kThreads, 0, a.stream>>>(p);
-  gs_back_carry_kernel<T>
-      <<<dim3((unsigned)ceil_div(a.D, 128), (unsigned)rows), 128, 0, a.stream>>>(p);
-  gs_back_apply_kernel<T><<<grid, kThreads, 0, a.stream>>>(p);
-  if (a.cu != nullptr && b.dh_in != nullptr)
-    gs_back_empty_kernel<<<512, 256, 0, a.stream>>>(a.cu, b.dh, b.dh_in, a.batch * a.D, a.D, bad);
-  gs_dlam_kernel<<<(unsigned)ceil_div(a.D, 128), 128, 0, a.stream>>>(part, rows * nch, a.D, a.lam,
-                                                                    a.c, b.dlam, a.cu != nullptr ? bad : nullptr);
-  return cudaGetLastError();
+  Scan p;
+  // (a sequence without tokens hands its state's gradient on)
+  cudaError_t e = prepare(a, w.scan, a.ws, b.dh, b.dh, b.dh_in, &p);
+  if (e != cudaSuccess) return e;
+  float *carry = reinterpret_cast<float *>(a.ws + w.carry), *dl = reinterpret_cast<float *>(a.ws + w.dl);
+  if (packed)
+    e = a.z != nullptr ? launch<T, true, true>(b, p, ck, carry, dl)
+                       : launch<T, true, false>(b, p, ck, carry, dl);
+  else
+    e = a.z != nullptr ? launch<T, false, true>(b, p, ck, carry, dl)
+                       : launch<T, false, false>(b, p, ck, carry, dl);
+  if (e != cudaSuccess) return e;
+  const int width = p.nblk * kWidth;
+  const unsigned int *bad = packed ? p.bad : nullptr;
+  const float *from = dl;
+  float *to = reinterpret_cast<float *>(a.ws + w.sums);
+  for (int64_t n = w.partials;;) {
+    const int64_t m = ceil_div(n, kSumRows);
+    const bool last = m == 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ceil_div(width, 32), (unsigned)m, 1);
+    cfg.blockDim = dim3(32 * kSumGroups, 1, 1);
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, gs_sum_kernel, from, n, width, last ? b.dlam : to,
+                           last ? a.lam : (const float *)nullptr, a.c, a.D, bad);
+    if (e != cudaSuccess || last) break;
+    from = to;
+    to += m * width;
+    n = m;
+  }
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 size_t gated_scan_backward_workspace(int64_t rows, int64_t L, int D, int io, bool packed) {
-  const size_t n = (size_t)rows * (size_t)ceil_div(L, kGsChunk) * (size_t)D;
-  return 256 + align_up(5 * n * 4, 256) + gated_scan_workspace(rows, L, D, io, packed);
+  return back_plan(rows, L, D, io, packed).total;
 }
 
 cudaError_t gated_scan_backward(const GatedScanBackwardArgs &b) {
   return b.f.io == MAMBA2_BF16 ? backward<__nv_bfloat16>(b) : backward<float>(b);
+}
+
+cudaError_t take_gated_scan_backward_errors(unsigned int *out) {
+  unsigned int v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_gs_errors, sizeof(v));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_gs_errors, &zero, sizeof(zero));
+  *out = v;
+  return e;
+}
+
+cudaError_t set_gated_scan_backward_stall(unsigned int v) {
+  return cudaMemcpyToSymbol(g_gs_stall, &v, sizeof(v));
 }
 
 }  // namespace m2

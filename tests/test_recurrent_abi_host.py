@@ -62,14 +62,14 @@ def test_bad_dims(kw, want):
 
 
 def test_sizes():
-    assert m2.lib().mamba2_gated_scan_checkpoint_count(ctypes.byref(_dims()), 0) == 2 * 3 * 64
-    assert m2.lib().mamba2_gated_scan_checkpoint_count(ctypes.byref(_dims()), 1) == 3 * 64
+    assert m2.lib().mamba2_gated_scan_checkpoint_count(ctypes.byref(_dims()), 0) == 2 * 19 * 64
+    assert m2.lib().mamba2_gated_scan_checkpoint_count(ctypes.byref(_dims()), 1) == 19 * 64
     assert m2.lib().mamba2_gated_scan_checkpoint_count(ctypes.byref(_dims(seqlen=0)), 0) == 0
     small, large = _dims(seqlen=4096), _dims(seqlen=32768)
     for f in (m2.mamba2_gated_scan_workspace_size, m2.mamba2_gated_scan_backward_workspace_size):
         assert 0 < f(small) < f(large)
-    assert m2.gated_scan_checkpoints(_dims(), device="cpu").shape == (2, 3, 64)
-    assert m2.gated_scan_checkpoints(_dims(), packed=True, device="cpu").shape == (1, 3, 64)
+    assert m2.gated_scan_checkpoints(_dims(), device="cpu").shape == (2, 19, 64)
+    assert m2.gated_scan_checkpoints(_dims(), packed=True, device="cpu").shape == (1, 19, 64)
 
 
 SHARED = [dict(lam=None), dict(lam=A0 + 2), dict(x=None), dict(r=None), dict(g=None),
