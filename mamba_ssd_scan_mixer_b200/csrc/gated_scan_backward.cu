@@ -26,13 +26,15 @@ namespace {
 static_assert(kGsChunk == 16, "tokens of a thread, between checkpoints");
 
 // ---------------------------------------------------------------- E at the chunks' ends
-template <typename T, bool GATED> using CarryTiles = Shared<T, GATED ? 3 : 2, 64>;
-template <typename T, bool GATED>
-constexpr int kCarryResident = sizeof(T) == 2 ? (GATED ? 4 : 5) : (GATED ? 2 : 3);
+// Nothing of a token is kept, so that a thread takes two chunks where shared memory lets
+// it: fewer tiles to look up.
+template <typename T> constexpr int kCarryTile = sizeof(T) == 2 ? 128 : 64;
+template <typename T, bool GATED> using CarryTiles = Shared<T, GATED ? 3 : 2, kCarryTile<T>>;
+template <bool GATED> constexpr int kCarryResident = GATED ? 2 : 3;
 
 __device__ __forceinline__ F2 silu2(F2 z) { return mul2(z, sigmoid2(z)); }
 
-// The map of a thread's 16 tokens, last to first.  `lasts`: the tokens that end a sequence.
+// The map of 16 tokens, last to first.  `lasts`: the tokens that end a sequence.
 template <typename S, bool FULL, bool RESETS, bool NEAR, bool GATED>
 __device__ __forceinline__ float4 back_map(const unsigned char *in, const int *marks,
                                            unsigned int lasts, F2 ncs, int n, const float *dh,
@@ -40,7 +42,7 @@ __device__ __forceinline__ float4 back_map(const unsigned char *in, const int *m
   using T = typename S::T;
   F2 A = f2(1.0f), E = f2(0.0f);
 #pragma unroll
-  for (int i = S::kTokens - 1; i >= 0; --i) {
+  for (int i = kGsChunk - 1; i >= 0; --i) {
     if (!FULL && i >= n) continue;
     const unsigned char *row = in + i * S::kRow;
     F2 a, less, dy = gs_pair<T>(row + S::kTensor);
@@ -63,7 +65,7 @@ __device__ __forceinline__ float4 back_map(const unsigned char *in, const int *m
 }
 
 template <typename T, bool PACKED, bool GATED>
-__global__ void __launch_bounds__(kThreads, (kCarryResident<T, GATED>))
+__global__ void __launch_bounds__(kThreads, (kCarryResident<GATED>))
     gs_back_carry_kernel(const __grid_constant__ Maps maps, const Scan p, const float *dh,
                          float *carry) {
   using S = CarryTiles<T, GATED>;
@@ -87,24 +89,36 @@ __global__ void __launch_bounds__(kThreads, (kCarryResident<T, GATED>))
     const int d = q.cb * kWidth + 2 * lane;
     const float2 ncs = *reinterpret_cast<const float2 *>(&sm.ncs[s][2 * lane]);
     const F2 k = f2(ncs.x, ncs.y);
-    const unsigned char *in = sm.in[s] + first * S::kRow + lane * (2 * (int)sizeof(T));
-    const int *marks = sm.marks[s] + first;
-    unsigned int lasts = 0;
-    if (PACKED)
-      lasts = __ballot_sync(0xffffffffu, lane < min(S::kTokens, n - first) && (marks[lane] & kLast));
-    float4 map;
-    if (__all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f) && lasts == 0 && n == S::kTile)
-      map = back_map<S, true, false, true, GATED>(in, marks, 0, k, n - first, dh, p.D, d);
-    else
-      map = back_map<S, false, PACKED, false, GATED>(in, marks, lasts, k, n - first, dh, p.D, d);
+    constexpr int kChunks = S::kTokens / kGsChunk;  // of a thread
+    float4 maps_of[kChunks], map;
+    const bool close = __all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f) && n == S::kTile;
+#pragma unroll
+    for (int c = kChunks - 1; c >= 0; --c) {
+      const int at = first + c * kGsChunk;
+      const unsigned char *in = sm.in[s] + at * S::kRow + lane * (2 * (int)sizeof(T));
+      const int *marks = sm.marks[s] + at;
+      unsigned int lasts = 0;
+      if (PACKED)
+        lasts = __ballot_sync(0xffffffffu, lane < min(kGsChunk, n - at) && (marks[lane] & kLast));
+      maps_of[c] = close && lasts == 0
+                       ? back_map<S, true, false, true, GATED>(in, marks, 0, k, n - at, dh, p.D, d)
+                       : back_map<S, false, PACKED, false, GATED>(in, marks, lasts, k, n - at, dh,
+                                                                  p.D, d);
+      map = c == kChunks - 1 ? maps_of[c] : gs_then(map, maps_of[c]);
+    }
     sm.seg[half][warp][lane] = map;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.segs[half]);
     float2 e;
     if (!exchange<PACKED>(sm, p, q, half, warp, lane, map, &e)) return;
-    if (d < p.D && first < n)
-      *reinterpret_cast<float2 *>(
-          carry + ((int64_t)q.row * nch + (t0 + first) / kGsChunk) * p.D + d) = e;
+#pragma unroll
+    for (int c = kChunks - 1; c >= 0; --c) {
+      const int at = first + c * kGsChunk;
+      if (d < p.D && at < n)
+        *reinterpret_cast<float2 *>(carry + ((int64_t)q.row * nch + (t0 + at) / kGsChunk) * p.D +
+                                    d) = e;
+      e = gs_through(maps_of[c], e);
+    }
   }
 }
 
@@ -131,7 +145,7 @@ template <typename T, bool GATED>
 constexpr int kApplyResident = GATED ? 2 : 3;
 
 template <typename T> struct Apply {
-  Scan p;
+  Scan p;  // (steps and tiles: of kApplyTile tokens)
   const float *ck, *carry;  // [rows][chunks][D]
   const float *h_in, *dh;   // packed rows: the sequences' initial states and final gradients
   T *dx, *dr, *dg, *dz;
@@ -139,17 +153,36 @@ template <typename T> struct Apply {
   unsigned long long zero;
 };
 
+// A state kept where a token's r and g were (each thread's own words).
+template <typename T> __device__ __forceinline__ void put_state(unsigned char *r, unsigned char *g, F2 h);
+template <> __device__ __forceinline__ void put_state<__nv_bfloat16>(unsigned char *r, unsigned char *g, F2 h) {
+  const float2 v = unpack(h);
+  *reinterpret_cast<float *>(r) = v.x;
+  *reinterpret_cast<float *>(g) = v.y;
+}
+template <> __device__ __forceinline__ void put_state<float>(unsigned char *r, unsigned char *, F2 h) {
+  *reinterpret_cast<float2 *>(r) = unpack(h);
+}
+template <typename T> __device__ __forceinline__ F2 get_state(const unsigned char *r, const unsigned char *g);
+template <> __device__ __forceinline__ F2 get_state<__nv_bfloat16>(const unsigned char *r, const unsigned char *g) {
+  return f2(*reinterpret_cast<const float *>(r), *reinterpret_cast<const float *>(g));
+}
+template <> __device__ __forceinline__ F2 get_state<float>(const unsigned char *r, const unsigned char *) {
+  const float2 v = *reinterpret_cast<const float2 *>(r);
+  return f2(v.x, v.y);
+}
+
 // One warp's 16 tokens.  FAST: all of them there, no sequence begins or ends among them,
 // and decays near one.
 template <typename T, bool GATED, bool PACKED, bool FAST>
-__device__ __forceinline__ F2 apply_tokens(const ApplyShared<T, GATED> &sm, int s,
+__device__ __forceinline__ F2 apply_tokens(ApplyShared<T, GATED> &sm, int s,
                                            const Apply<T> &q, int row, int64_t t0, int n, int first,
                                            int lane, int d) {
   using S = ApplyShared<T, GATED>;
   constexpr int K = kGsChunk, kTensor = S::kTensor;
   const Scan &p = q.p;
   const int warp = first / K;
-  const unsigned char *in = sm.in[s] + first * S::kRow + lane * (2 * (int)sizeof(T));
+  unsigned char *in = sm.in[s] + first * S::kRow + lane * (2 * (int)sizeof(T));
   const int *marks = sm.marks[s] + first;
   const float2 nn = *reinterpret_cast<const float2 *>(&sm.ncs[s][2 * lane]);
   const F2 ncs = f2(nn.x, nn.y);
@@ -158,7 +191,7 @@ __device__ __forceinline__ F2 apply_tokens(const ApplyShared<T, GATED> &sm, int 
   F2 h = f2(h0.x, h0.y), e = f2(e0.x, e0.y), dl = f2(0.0f);
   const bool real = d < p.D;
   const int count = FAST ? K : min(K, n - first);
-  F2 R[K], G[K], before[K];
+  F2 R[K], G[K];
 #pragma unroll
   for (int i = 0; i < K; ++i) {
     if (!FAST && i >= count) continue;
@@ -169,19 +202,24 @@ __device__ __forceinline__ F2 apply_tokens(const ApplyShared<T, GATED> &sm, int 
         h = f2(v.x, v.y);
       }
     }
-    const unsigned char *at = in + i * S::kRow;
+    unsigned char *at = in + i * S::kRow;
     const Coeffs c = coefficients<FAST>(gs_pair<T>(at), gs_clamped<T>(at + kTensor),
                                         gs_clamped<T>(at + 2 * kTensor), ncs);
     R[i] = c.R;
     G[i] = c.G;
-    before[i] = h;
+    put_state<T>(at + kTensor, at + 2 * kTensor, h);
     h = fma2(c.a, h, c.b);
   }
-  // R, G and h alone are kept: the rest is cheaper made again than held.  (The compiler
-  // would hold it, in local memory; it does not know that `zero` is zero.)
+  // R and G are kept in registers and h where r and g were: the rest is cheaper made again
+  // than held.  (The compiler would hold it, in local memory; it does not know that `zero`
+  // is zero.)
   const F2 ncs2 = F2{ncs.v ^ q.zero};
   in += q.zero;
-  const int64_t out0 = ((int64_t)row * p.L + t0 + first) * p.D + d;
+  // the same for every lane, and 32-bit offsets from there
+  const int64_t tile0 = ((int64_t)row * p.L + t0) * p.D + (d - 2 * lane);
+  T *const dx_out = q.dx + tile0, *const dr_out = q.dr + tile0, *const dg_out = q.dg + tile0;
+  T *const dz_out = GATED ? q.dz + tile0 : nullptr;
+  const uint32_t off0 = (uint32_t)first * p.D + 2 * lane;
 #pragma unroll
   for (int i = K - 1; i >= 0; --i) {
     if (!FAST && i >= count) continue;
@@ -190,18 +228,18 @@ __device__ __forceinline__ F2 apply_tokens(const ApplyShared<T, GATED> &sm, int 
     F2 dy = gs_pair<T>(at + 3 * kTensor), a, less;
     const F2 t = mul2(ncs2, R[i]);
     decay2<FAST>(t, &a, &less);
-    constexpr float down = 1.0f / kGateScale, down2 = down * down;
-    const F2 more = fma2(a, f2(-1.0f), f2(-1.0f));
-    const float2 v = unpack(mul2(less, more)), w = unpack(mul2(less, mul2(more, f2(down2))));
-    const float m0 = sqrt_ap(w.x), m1 = sqrt_ap(w.y);
-    const F2 mG = mul2(f2(m0, m1), G[i]);
+    constexpr float down = 1.0f / kGateScale, down2 = down * down, up2 = kGateScale * kGateScale;
+    const F2 vv = mul2(less, fma2(a, f2(-1.0f), f2(-1.0f)));
+    const float2 v = unpack(vv), w = unpack(mul2(vv, f2(down2)));
+    const F2 before = get_state<T>(at + kTensor, at + 2 * kTensor);
+    const F2 mG = mul2(f2(sqrt_ap(w.x), sqrt_ap(w.y)), G[i]);
     const F2 b = mul2(mG, x);
     if (GATED) {
       const F2 z = gs_pair<T>(at + 4 * kTensor), sig = sigmoid2(z);
-      const F2 ht = fma2(a, before[i], b);
+      const F2 ht = fma2(a, before, b);
       // silu' = sig (1 + z (1 - sig))
       const F2 slope = mul2(sig, fma2(z, fma2(sig, f2(-1.0f), f2(1.0f)), f2(1.0f)));
-      if (real) st2(q.dz + out0 + (int64_t)i * p.D, unpack(mul2(mul2(dy, ht), slope)));
+      if (real) st2(dz_out + (off0 + i * p.D), unpack(mul2(mul2(dy, ht), slope)));
       dy = mul2(dy, mul2(z, sig));
     }
     if (!FAST && PACKED && (marks[i] & kLast)) {
@@ -215,18 +253,18 @@ __device__ __forceinline__ F2 apply_tokens(const ApplyShared<T, GATED> &sm, int 
     const F2 dx = mul2(dd, mG);
     const F2 dg = mul2(mul2(dx, x), fma2(G[i], f2(-down), f2(1.0f)));
     // where v is next to nothing m, and b with it, was taken for zero: so is b / v
-    const F2 iv = f2(rcp(max_nan(v.x, 1.3e-17f)), rcp(max_nan(v.y, 1.3e-17f)));
+    const F2 iv = f2(rcp(-max_nan(v.x, 1.3e-17f)), rcp(-max_nan(v.y, 1.3e-17f)));  // -1 / v
     e = mul2(a, dd);
-    const F2 dla = mul2(e, fma2(mul2(a, b), mul2(iv, f2(-1.0f)), before[i]));
+    const F2 dla = mul2(e, fma2(mul2(a, b), iv, before));
     dl = fma2(dla, R[i], dl);
-    const F2 dr = mul2(mul2(dla, mul2(t, f2(0.6931471805599453f))), fma2(R[i], f2(-1.0f), f2(1.0f)));
+    // (|la| < 2^-56 is flushed on the way: a gate so shut, r = -inf, gets no gradient)
+    const F2 dr = mul2(dla, mul2(mul2_flush(t, f2(0.6931471805599453f * down2)),
+                                 fma2(R[i], f2(-up2), f2(up2))));
     if (real) {
-      const int64_t o = out0 + (int64_t)i * p.D;
-      st2(q.dx + o, unpack(dx));
-      // a gate so shut that m counts as zero (r = -inf) gets no gradient
-      const float2 g = unpack(dr);
-      st2(q.dr + o, m0 == 0.0f ? 0.0f : g.x, m1 == 0.0f ? 0.0f : g.y);
-      st2(q.dg + o, unpack(dg));
+      const uint32_t o = off0 + i * p.D;
+      st2(dx_out + o, unpack(dx));
+      st2(dr_out + o, unpack(dr));
+      st2(dg_out + o, unpack(dg));
     }
     if (!FAST && PACKED && (marks[i] & kFirst) && q.dh_in != nullptr && real)
       *reinterpret_cast<float2 *>(q.dh_in + (int64_t)(marks[i] >> 2) * p.D + d) = unpack(e);
@@ -299,6 +337,7 @@ __global__ void __launch_bounds__(kApplyThreads, (kApplyResident<T, GATED>))
         dl = apply_tokens<T, GATED, PACKED, false>(sm, s, q, row, t0, n, first, lane, d);
     }
     sm.dl[half][warp][lane] = unpack(dl);
+    fence_proxy_async_smem();  // the states written into the stage, before copies come there
     segments_done();  // every warp is done with the stage
     if (*reinterpret_cast<volatile int *>(&sm.dead)) {
       // what this block has under way lands before it leaves
@@ -356,10 +395,11 @@ struct BackPlan {
 };
 BackPlan back_plan(int64_t rows, int64_t L, int D, int io, bool packed) {
   BackPlan b;
-  b.scan = plan_of(rows, L, D, kApplyTile, packed);
+  b.scan = plan_of(rows, L, D, io == MAMBA2_BF16 ? kCarryTile<__nv_bfloat16> : kCarryTile<float>,
+                   packed);
   const size_t chunks = (size_t)(rows * ceil_div(L, kGsChunk)) * D * 4;
   const size_t width = (size_t)b.scan.nblk * kWidth * 4;
-  b.partials = rows * b.scan.steps;
+  b.partials = rows * ceil_div(L, kApplyTile);
   b.carry = align_up(b.scan.total, 256);
   b.ck = b.carry + align_up(chunks, 256);
   b.dl = b.ck + align_up(chunks, 256);
@@ -380,16 +420,17 @@ cudaError_t launch(const GatedScanBackwardArgs &b, const Scan &p, const float *c
   for (int k = 0; k < (GATED ? 5 : 4); ++k)
     if (!gs_tensor_map(&apply.m[k], a.io, in[k], rows, a.L, a.D, ld[k], kApplyTile))
       return cudaErrorInvalidValue;
-  back.m[0] = apply.m[1];
-  back.m[1] = apply.m[3];
-  back.m[2] = apply.m[4];
+  constexpr int kOf[3] = {1, 3, 4};  // r, dy, z
+  for (int k = 0; k < (GATED ? 3 : 2); ++k)
+    if (!gs_tensor_map(&back.m[k], a.io, in[kOf[k]], rows, a.L, a.D, ld[kOf[k]], kCarryTile<T>))
+      return cudaErrorInvalidValue;
   {
     constexpr size_t smem = sizeof(CarryTiles<T, GATED>);
-    static_assert((kCarryResident<T, GATED>)*(smem + 1024 + 256) <= 228 * 1024, "blocks to an SM");
+    static_assert((kCarryResident<GATED>)*(smem + 1024 + 256) <= 228 * 1024, "blocks to an SM");
     static ContextOnce once;
     const cudaError_t e = launch_dependent(
         gs_back_carry_kernel<T, PACKED, GATED>, once,
-        std::min(p.tiles, kCarryResident<T, GATED> * sm_count()), kThreads, smem, a.stream, back, p,
+        std::min(p.tiles, kCarryResident<GATED> * sm_count()), kThreads, smem, a.stream, back, p,
         b.dh, carry);
     if (e != cudaSuccess) return e;
   }
@@ -398,6 +439,8 @@ cudaError_t launch(const GatedScanBackwardArgs &b, const Scan &p, const float *c
   static ContextOnce once;
   Apply<T> q;
   q.p = p;
+  q.p.steps = (int)ceil_div(a.L, kApplyTile);
+  q.p.tiles = (int)(rows * q.p.steps * p.nblk);
   q.ck = ck;
   q.carry = carry;
   q.h_in = b.h_in;
@@ -410,7 +453,7 @@ cudaError_t launch(const GatedScanBackwardArgs &b, const Scan &p, const float *c
   q.dl = dl;
   q.zero = 0;
   return launch_dependent(gs_back_apply_kernel<T, PACKED, GATED>, once,
-                          std::min(p.tiles, kApplyResident<T, GATED> * sm_count()), kApplyThreads, smem,
+                          std::min(q.p.tiles, kApplyResident<T, GATED> * sm_count()), kApplyThreads, smem,
                           a.stream, apply, q);
 }
 
