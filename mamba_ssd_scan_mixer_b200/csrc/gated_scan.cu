@@ -1,6 +1,6 @@
 // Prefill and decode step of the gated linear recurrence (gated_scan.cuh).
 //
-// Prefill reads every input once.  A tile is 64 (fp32: 32) tokens of 64 channels of a
+// Prefill reads every input once.  A tile is 128 (fp32: 64) tokens of 32 channels of a
 // row; resident blocks take tiles in order, all channels of a stretch of tokens before
 // the next stretch, from a counter:
 //   1. the tile's x, r and g arrive by TMA, two tiles ahead of the arithmetic;
@@ -27,7 +27,7 @@ namespace {
 // Blocks on an SM at once, and tokens of a tile: what registers and shared memory hold.
 template <bool GATED> constexpr int kResident = GATED ? 3 : 4;
 template <typename T, bool GATED>
-using Tiles = Shared<T, GATED ? 4 : 3, sizeof(T) == 2 ? 64 : 32>;
+using Tiles = Shared<T, GATED ? 4 : 3, sizeof(T) == 2 ? 128 : 64>;
 
 // Step 2: a and b of the thread's tokens, and their composition.  `begins`: the tokens (a
 // bit each) that begin a sequence of packed rows.
@@ -80,14 +80,15 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
   using S = Tiles<T, GATED>;
   extern __shared__ __align__(128) unsigned char raw[];
   S &sm = *reinterpret_cast<S *>(raw);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5;
   if (!begin<S, PACKED>(sm, p)) return;
   if (warp == kWarps) {
     look_up<S, PACKED, false>(sm, maps, p);
     return;
   }
 
-  const int first = warp * S::kTokens;
+  const int lane = threadIdx.x % kLanes, seg = threadIdx.x / kLanes;  // of a half warp
+  const int first = seg * S::kTokens;
   for (int it = 0;; ++it) {
     const int s = it % S::kStages, half = it & 1;
     if (!mbar_wait_parked(&sm.full[s], (it / S::kStages) & 1, &g_gs_errors)) sm.dead = 1;
@@ -102,20 +103,24 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
     const int *marks = sm.marks[s] + first;
     // packed rows: which of the warp's tokens begin and end a sequence
     unsigned int begins = 0, ends = 0;
+    bool whole = true;  // (no sequence begins in either half)
     if (PACKED) {
-      const int mark = lane < min(S::kTokens, n - first) ? marks[lane] : 0;
+      const int mark = lane < min(S::kTokens, n - first) ? marks[lane] : 0, up = threadIdx.x & 16;
       begins = __ballot_sync(0xffffffffu, mark & kFirst);
       ends = __ballot_sync(0xffffffffu, h_out != nullptr && (mark & kLast));
+      whole = begins == 0;
+      begins = begins >> up & 0xffff;
+      ends = ends >> up & 0xffff;
     }
     const F2 k = f2(ncs.x, ncs.y);
     float4 map;
-    if (__all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f) && begins == 0)
+    if (__all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f) && whole)
       map = n == S::kTile
                 ? make_maps<S, true, false, true>(in, marks, 0, k, n - first, p, d, a, b)
                 : make_maps<S, false, false, true>(in, marks, 0, k, n - first, p, d, a, b);
     else
       map = make_maps<S, false, PACKED, false>(in, marks, begins, k, n - first, p, d, a, b);
-    sm.seg[half][warp][lane] = map;
+    sm.seg[half][seg][lane] = map;
     typename Pair<T>::V gate[GATED ? S::kTokens : 1];
     if (GATED) {
 #pragma unroll
@@ -123,10 +128,10 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
         gate[i] = *reinterpret_cast<const typename Pair<T>::V *>(in + i * S::kRow + 3 * S::kTensor);
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.segs[half]);
+    if (threadIdx.x % 32 == 0) mbar_arrive(&sm.segs[half]);
     const int64_t token = (int64_t)q.row * p.L + t0 + first;
     float2 h;
-    if (!exchange<PACKED>(sm, p, q, half, warp, lane, map, &h)) return;
+    if (!exchange<PACKED>(sm, p, q, half, seg, lane, map, &h)) return;
     if (ck != nullptr && real && first % kGsChunk == 0 && first < n)
       *reinterpret_cast<float2 *>(
           ck + ((int64_t)q.row * ((p.L + kGsChunk - 1) / kGsChunk) + (t0 + first) / kGsChunk) * p.D +
@@ -221,7 +226,8 @@ template <typename T> cudaError_t prefill(const GatedScanArgs &a) {
   const void *in[4] = {a.x, a.r, a.g, a.z};
   const int64_t ld[4] = {a.ld_x, a.ld_r, a.ld_g, a.ld_z};
   for (int k = 0; k < (gated ? 4 : 3); ++k)
-    if (!gs_tensor_map(&m.m[k], a.io, in[k], rows, a.L, a.D, ld[k], Tiles<T, false>::kTile))
+    if (!gs_tensor_map(&m.m[k], a.io, in[k], rows, a.L, a.D, ld[k], kWidth,
+                       Tiles<T, false>::kTile))
       return cudaErrorInvalidValue;
   Scan p;
   // (a sequence without tokens keeps its state, or starts and ends at zero)
@@ -243,7 +249,7 @@ template <typename T> cudaError_t step(const GatedScanArgs &a) {
 }  // namespace
 
 bool gs_tensor_map(CUtensorMap *m, int io, const void *base, int64_t rows, int64_t L, int D,
-                   int64_t ld, int tokens) {
+                   int64_t ld, int width, int tokens) {
   using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                               const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
                               const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -264,7 +270,7 @@ bool gs_tensor_map(CUtensorMap *m, int io, const void *base, int64_t rows, int64
   const uint64_t esz = bf ? 2 : 4;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)L, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {(uint64_t)ld * esz, (uint64_t)ld * esz * (uint64_t)L};
-  const cuuint32_t box[3] = {64, (cuuint32_t)tokens, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)width, (cuuint32_t)tokens, 1};
   const cuuint32_t one[3] = {1, 1, 1};
   return encode(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
                 const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,

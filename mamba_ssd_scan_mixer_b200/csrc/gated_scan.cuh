@@ -55,9 +55,9 @@ cudaError_t take_gated_scan_errors(unsigned int *out);
 cudaError_t set_gated_scan_stall(unsigned int v);
 cudaError_t take_gated_scan_backward_errors(unsigned int *out);
 cudaError_t set_gated_scan_backward_stall(unsigned int v);
-// Tiles of 32 tokens and 64 channels in a call: they are counted in 32 bits.
+// Tiles of 64 tokens and 32 channels in a call: they are counted in 32 bits.
 inline int64_t gs_tiles(int64_t rows, int64_t L, int64_t D) {
-  return rows * ceil_div(L, 32) * ceil_div(D, 64);
+  return rows * ceil_div(L, 64) * ceil_div(D, 32);
 }
 
 // ---------------------------------------------------------------- arithmetic
@@ -254,10 +254,10 @@ struct ContextOnce {
   }
 };
 
-// [rows][L][D] with a token stride of ld elements, in boxes of `tokens` by 64 channels;
-// false if it cannot be described.
+// [rows][L][D] with a token stride of ld elements, in boxes of `tokens` by `width`
+// channels; false if it cannot be described.
 bool gs_tensor_map(CUtensorMap *m, int io, const void *base, int64_t rows, int64_t L, int D,
-                   int64_t ld, int tokens);
+                   int64_t ld, int width, int tokens);
 
 // Records that blocks pass to one another.  A word that has not been written holds
 // kUnset, a NaN that no arithmetic gives, so that each word tells by itself whether it is

@@ -28,7 +28,7 @@ static_assert(kGsChunk == 16, "tokens of a thread, between checkpoints");
 // ---------------------------------------------------------------- E at the chunks' ends
 // Nothing of a token is kept, so that a thread takes two chunks where shared memory lets
 // it: fewer tiles to look up.
-template <typename T> constexpr int kCarryTile = sizeof(T) == 2 ? 128 : 64;
+template <typename T> constexpr int kCarryTile = sizeof(T) == 2 ? 256 : 128;
 template <typename T, bool GATED> using CarryTiles = Shared<T, GATED ? 3 : 2, kCarryTile<T>>;
 template <bool GATED> constexpr int kCarryResident = GATED ? 2 : 3;
 
@@ -71,14 +71,14 @@ __global__ void __launch_bounds__(kThreads, (kCarryResident<GATED>))
   using S = CarryTiles<T, GATED>;
   extern __shared__ __align__(128) unsigned char raw[];
   S &sm = *reinterpret_cast<S *>(raw);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (!begin<S, PACKED>(sm, p)) return;
   launch_dependents();
-  if (warp == kWarps) {
+  if (threadIdx.x >= 32 * kWarps) {
     look_up<S, PACKED, true>(sm, maps, p);
     return;
   }
-  const int first = (kWarps - 1 - warp) * S::kTokens;  // of the warp's tokens
+  const int lane = threadIdx.x % kLanes, seg = threadIdx.x / kLanes;  // of a half warp
+  const int first = (kSegs - 1 - seg) * S::kTokens;
   const int64_t nch = (p.L + kGsChunk - 1) / kGsChunk;
   for (int it = 0;; ++it) {
     const int s = it % S::kStages, half = it & 1;
@@ -100,17 +100,19 @@ __global__ void __launch_bounds__(kThreads, (kCarryResident<GATED>))
       unsigned int lasts = 0;
       if (PACKED)
         lasts = __ballot_sync(0xffffffffu, lane < min(kGsChunk, n - at) && (marks[lane] & kLast));
-      maps_of[c] = close && lasts == 0
+      const bool whole = lasts == 0;  // (no sequence ends in either half)
+      lasts = lasts >> (threadIdx.x & 16) & 0xffff;
+      maps_of[c] = close && whole
                        ? back_map<S, true, false, true, GATED>(in, marks, 0, k, n - at, dh, p.D, d)
                        : back_map<S, false, PACKED, false, GATED>(in, marks, lasts, k, n - at, dh,
                                                                   p.D, d);
       map = c == kChunks - 1 ? maps_of[c] : gs_then(map, maps_of[c]);
     }
-    sm.seg[half][warp][lane] = map;
+    sm.seg[half][seg][lane] = map;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.segs[half]);
+    if (threadIdx.x % 32 == 0) mbar_arrive(&sm.segs[half]);
     float2 e;
-    if (!exchange<PACKED>(sm, p, q, half, warp, lane, map, &e)) return;
+    if (!exchange<PACKED>(sm, p, q, half, seg, lane, map, &e)) return;
 #pragma unroll
     for (int c = kChunks - 1; c >= 0; --c) {
       const int at = first + c * kGsChunk;
@@ -123,18 +125,18 @@ __global__ void __launch_bounds__(kThreads, (kCarryResident<GATED>))
 }
 
 // ---------------------------------------------------------------- the gradients
-constexpr int kApplyTile = 64;
+constexpr int kApplyTile = 64, kApplyWidth = 64;  // whole 128-byte lines of bf16
 
 template <typename T, bool GATED> struct ApplyShared {
   static constexpr int kTensors = GATED ? 5 : 4;
   // one stage where two would leave too few blocks to an SM
   static constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
-  static constexpr int kRow = kWidth * (int)sizeof(T), kTensor = kApplyTile * kRow;
+  static constexpr int kRow = kApplyWidth * (int)sizeof(T), kTensor = kApplyTile * kRow;
   alignas(128) unsigned char in[kStages][kTensors * kTensor];
-  alignas(16) float h[kStages][kWarps][kWidth];  // the states entering the warps' tokens
-  alignas(16) float e[kStages][kWarps][kWidth];  // and the E
+  alignas(16) float h[kStages][kWarps][kApplyWidth];  // the states entering the warps' tokens
+  alignas(16) float e[kStages][kWarps][kApplyWidth];  // and the E
   alignas(16) int marks[kStages][kApplyTile];
-  alignas(16) float ncs[kStages][kWidth];
+  alignas(16) float ncs[kStages][kApplyWidth];
   float2 dl[2][kWarps][32];
   uint64_t full[kStages];
   int dead;  // a wait ran out: everybody leaves after the tile
@@ -145,7 +147,7 @@ template <typename T, bool GATED>
 constexpr int kApplyResident = GATED ? 2 : 3;
 
 template <typename T> struct Apply {
-  Scan p;  // (steps and tiles: of kApplyTile tokens)
+  Scan p;  // (steps, nblk and tiles: of kApplyTile tokens and kApplyWidth channels)
   const float *ck, *carry;  // [rows][chunks][D]
   const float *h_in, *dh;   // packed rows: the sequences' initial states and final gradients
   T *dx, *dr, *dg, *dz;
@@ -299,19 +301,19 @@ __global__ void __launch_bounds__(kApplyThreads, (kApplyResident<T, GATED>))
     const int cb = tile % p.nblk, row = tile / p.nblk % p.rows;
     const int t0 = tile / p.nblk / p.rows * kApplyTile;
     const int n = (int)min((int64_t)kApplyTile, p.L - t0), chunks = (n + kGsChunk - 1) / kGsChunk;
-    const uint32_t wide = (uint32_t)min(kWidth, p.D - cb * kWidth) * 4;
+    const uint32_t wide = (uint32_t)min(kApplyWidth, p.D - cb * kApplyWidth) * 4;
     const uint32_t mark_bytes = PACKED ? (n * 4 + 15) / 16 * 16 : 0;
-    mbar_arrive_expect_tx(&sm.full[s], S::kTensors * S::kTensor + 2 * chunks * wide + kWidth * 4 +
+    mbar_arrive_expect_tx(&sm.full[s], S::kTensors * S::kTensor + 2 * chunks * wide + kApplyWidth * 4 +
                                            mark_bytes);
 #pragma unroll
     for (int k = 0; k < S::kTensors; ++k)
-      tma_load_3d(sm.in[s] + k * S::kTensor, &maps.m[k], cb * kWidth, t0, row, &sm.full[s]);
-    const int64_t at = ((int64_t)row * nch + t0 / kGsChunk) * p.D + cb * kWidth;
+      tma_load_3d(sm.in[s] + k * S::kTensor, &maps.m[k], cb * kApplyWidth, t0, row, &sm.full[s]);
+    const int64_t at = ((int64_t)row * nch + t0 / kGsChunk) * p.D + cb * kApplyWidth;
     for (int k = 0; k < chunks; ++k) {
       bulk_g2s(sm.h[s][k], q.ck + at + (int64_t)k * p.D, wide, &sm.full[s]);
       bulk_g2s(sm.e[s][k], q.carry + at + (int64_t)k * p.D, wide, &sm.full[s]);
     }
-    bulk_g2s(sm.ncs[s], p.ncs + cb * kWidth, kWidth * 4, &sm.full[s]);
+    bulk_g2s(sm.ncs[s], p.ncs + cb * kApplyWidth, kApplyWidth * 4, &sm.full[s]);
     if (PACKED) bulk_g2s(sm.marks[s], p.marks + t0, mark_bytes, &sm.full[s]);
   };
   constexpr int kFetcher = 32 * kWarps - 1;
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(kApplyThreads, (kApplyResident<T, GATED>))
     if (!there) sm.dead = 1;
     const int cb = tile % p.nblk, row = tile / p.nblk % p.rows, step = tile / p.nblk / p.rows;
     const int t0 = step * kApplyTile, n = (int)min((int64_t)kApplyTile, p.L - t0);
-    const int d = cb * kWidth + 2 * lane;
+    const int d = cb * kApplyWidth + 2 * lane;
     F2 dl = f2(0.0f);
     if (there && first < n) {
       const float2 nn = *reinterpret_cast<const float2 *>(&sm.ncs[s][2 * lane]);
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(kApplyThreads, (kApplyResident<T, GATED>))
         v.y += sm.dl[half][k][lane].y;
       }
       *reinterpret_cast<float2 *>(
-          q.dl + ((int64_t)row * p.steps + step) * (p.nblk * kWidth) + d) = v;
+          q.dl + ((int64_t)row * p.steps + step) * (p.nblk * kApplyWidth) + d) = v;
     }
   }
 }
@@ -398,7 +400,7 @@ BackPlan back_plan(int64_t rows, int64_t L, int D, int io, bool packed) {
   b.scan = plan_of(rows, L, D, io == MAMBA2_BF16 ? kCarryTile<__nv_bfloat16> : kCarryTile<float>,
                    packed);
   const size_t chunks = (size_t)(rows * ceil_div(L, kGsChunk)) * D * 4;
-  const size_t width = (size_t)b.scan.nblk * kWidth * 4;
+  const size_t width = (size_t)ceil_div(D, kApplyWidth) * kApplyWidth * 4;
   b.partials = rows * ceil_div(L, kApplyTile);
   b.carry = align_up(b.scan.total, 256);
   b.ck = b.carry + align_up(chunks, 256);
@@ -418,11 +420,11 @@ cudaError_t launch(const GatedScanBackwardArgs &b, const Scan &p, const float *c
   const int64_t ld[5] = {a.ld_x, a.ld_r, a.ld_g, a.D, a.ld_z};
   Maps apply = {}, back = {};
   for (int k = 0; k < (GATED ? 5 : 4); ++k)
-    if (!gs_tensor_map(&apply.m[k], a.io, in[k], rows, a.L, a.D, ld[k], kApplyTile))
+    if (!gs_tensor_map(&apply.m[k], a.io, in[k], rows, a.L, a.D, ld[k], kApplyWidth, kApplyTile))
       return cudaErrorInvalidValue;
   constexpr int kOf[3] = {1, 3, 4};  // r, dy, z
   for (int k = 0; k < (GATED ? 3 : 2); ++k)
-    if (!gs_tensor_map(&back.m[k], a.io, in[kOf[k]], rows, a.L, a.D, ld[kOf[k]], kCarryTile<T>))
+    if (!gs_tensor_map(&back.m[k], a.io, in[kOf[k]], rows, a.L, a.D, ld[kOf[k]], kWidth, kCarryTile<T>))
       return cudaErrorInvalidValue;
   {
     constexpr size_t smem = sizeof(CarryTiles<T, GATED>);
@@ -440,7 +442,8 @@ cudaError_t launch(const GatedScanBackwardArgs &b, const Scan &p, const float *c
   Apply<T> q;
   q.p = p;
   q.p.steps = (int)ceil_div(a.L, kApplyTile);
-  q.p.tiles = (int)(rows * q.p.steps * p.nblk);
+  q.p.nblk = (int)ceil_div(a.D, kApplyWidth);
+  q.p.tiles = (int)(rows * q.p.steps * q.p.nblk);
   q.ck = ck;
   q.carry = carry;
   q.h_in = b.h_in;
@@ -486,7 +489,7 @@ template <typename T> cudaError_t backward(const GatedScanBackwardArgs &b) {
     e = a.z != nullptr ? launch<T, false, true>(b, p, ck, carry, dl)
                        : launch<T, false, false>(b, p, ck, carry, dl);
   if (e != cudaSuccess) return e;
-  const int width = p.nblk * kWidth;
+  const int width = (int)ceil_div(a.D, kApplyWidth) * kApplyWidth;
   const unsigned int *bad = packed ? p.bad : nullptr;
   const float *from = dl;
   float *to = reinterpret_cast<float *>(a.ws + w.sums);

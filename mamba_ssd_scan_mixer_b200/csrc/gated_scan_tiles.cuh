@@ -13,8 +13,12 @@ static __device__ unsigned int g_gs_stall = 0;  // mamba2_debug_stall_waits
 
 namespace {
 
-constexpr int kWidth = 64;  // channels of a tile: two for each lane
-constexpr int kWarps = 4;   // that compute
+// Channels of a tile: half a warp takes two each.  (Wider tiles would be shorter: more of
+// a row's tiles, each waiting for the one before, would be under way at once.)
+constexpr int kWidth = 32;
+constexpr int kLanes = kWidth / 2;
+constexpr int kWarps = 4;           // that compute
+constexpr int kSegs = 2 * kWarps;   // segments of a tile's tokens: one for each half warp
 constexpr int kThreads = 32 * (kWarps + 1);
 // The state entering a tile is put together from that left by the `back`th tile before
 // it and the maps of those between, one after the other: E(t + 1) = A(t) E(t) + H(t),
@@ -33,14 +37,14 @@ struct Maps {
 };
 
 struct Scan {
-  const float *ncs;  // [nblk][64] -c softplus(lam) log2(e)
+  const float *ncs;  // -c softplus(lam) log2(e) of each channel, padded with zeros
   int64_t L;
   int D, nblk, steps, rows, tiles, back;  // steps: tiles along a row's tokens
   const int *marks;         // packed rows: [L], else null
   const unsigned int *bad;  // packed rows: wrong offsets
   const float *first;       // [rows][D] the states entering the rows, or null (packed: each sequence's)
-  float4 *maps;             // [tiles][32]: the tiles' maps
-  float2 *states;           // [tiles][32]: the states they leave
+  float4 *maps;             // [tiles][kLanes]: the tiles' maps
+  float2 *states;           // [tiles][kLanes]: the states they leave
   unsigned int *ticket;
 };
 
@@ -51,14 +55,14 @@ struct Tile {
 template <typename T_, int TENSORS, int TOKENS> struct Shared {
   using T = T_;
   static constexpr int kTensors = TENSORS, kTile = TOKENS, kStages = 2;
-  static constexpr int kTokens = TOKENS / kWarps;       // of a thread
+  static constexpr int kTokens = TOKENS / kSegs;        // of a thread
   static constexpr int kRow = kWidth * (int)sizeof(T);  // bytes of a token
   static constexpr int kTensor = kTile * kRow;
   alignas(128) unsigned char in[kStages][kTensors * kTensor];
   alignas(16) int marks[kStages][kTile];
   alignas(16) float ncs[kStages][kWidth];
-  float4 seg[2][kWarps][32];
-  float2 enter[2][32];
+  float4 seg[2][kSegs][kLanes];
+  float2 enter[2][kLanes];
   uint64_t full[kStages], segs[2];
   Tile tile[kStages];
   int dead;  // a wait ran out: everybody leaves after the next `entered`
@@ -74,7 +78,7 @@ __global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, uin
   launch_dependents();
   const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t all = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = at; i < (D + kWidth - 1) / kWidth * kWidth; i += all)
+  for (int64_t i = at; i < (D + 63) / 64 * 64; i += all)
     ncs[i] = i < D ? -c * softplus_f(lam[i]) * kLog2e : 0.0f;
   for (int64_t i = at; i < nrecords; i += all)
     records[i] = make_uint4(kUnset, kUnset, kUnset, kUnset);
@@ -132,18 +136,18 @@ template <typename S, bool PACKED> __device__ __forceinline__ bool begin(S &sm, 
   return !(PACKED && *p.bad);
 }
 
-// The segments before this warp's (in the order of the scan) as one map.
+// The segments before `seg` (in the order of the scan) as one map.
 template <bool PACKED, typename S>
-__device__ __forceinline__ float4 compose_before(const S &sm, int half, int warp, int lane) {
+__device__ __forceinline__ float4 compose_before(const S &sm, int half, int seg, int lane) {
   if (PACKED) {
     float4 pre = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-    for (int k = 0; k < warp; ++k) pre = gs_then(pre, sm.seg[half][k][lane]);
+    for (int k = 0; k < seg; ++k) pre = gs_then(pre, sm.seg[half][k][lane]);
     return pre;
   }
   F2 A = f2(1.0f), H = f2(0.0f);
 #pragma unroll
-  for (int k = 0; k < kWarps - 1; ++k)
-    if (k < warp) {
+  for (int k = 0; k < kSegs - 1; ++k)
+    if (k < seg) {
       const float4 m = sm.seg[half][k][lane];
       A = mul2(A, f2(m.x, m.y));
       H = fma2(f2(m.x, m.y), H, f2(m.z, m.w));
@@ -152,27 +156,28 @@ __device__ __forceinline__ float4 compose_before(const S &sm, int half, int warp
   return make_float4(x.x, x.y, y.x, y.y);
 }
 
-// Between the segments' maps and the states that enter them: the last warp publishes the
-// tile's map and the state it leaves; every warp gets the state entering its segment.
-// False if a wait ran out.
+// Between the segments' maps and the states that enter them: the last segment's threads
+// publish the tile's map and the state it leaves; every thread gets the state entering
+// its segment.  False if a wait ran out.
 template <bool PACKED, typename S>
-__device__ __forceinline__ bool exchange(S &sm, const Scan &p, const Tile &q, int half, int warp,
+__device__ __forceinline__ bool exchange(S &sm, const Scan &p, const Tile &q, int half, int seg,
                                          int lane, float4 map, float2 *h) {
   segments_done();
-  const float4 pre = compose_before<PACKED>(sm, half, warp, lane);
-  const int tile = (q.step * p.rows + q.row) * p.nblk + q.cb;
-  const bool tells = warp == kWarps - 1 && q.step < p.steps - 1;
-  if (tells) map = gs_then(pre, map);  // of the tile
-  if (tells && q.step > 0) record_put(p.maps + (int64_t)tile * 32 + lane, map);
+  const float4 pre = compose_before<PACKED>(sm, half, seg, lane);
+  const int64_t at = (int64_t)((q.step * p.rows + q.row) * p.nblk + q.cb) * kLanes + lane;
+  const bool tells = seg == kSegs - 1 && q.step < p.steps - 1;
+  if (tells) {
+    map = gs_then(pre, map);  // of the tile
+    if (q.step > 0) record_put(p.maps + at, map);
+  }
   entered_wait(half);
   if (*reinterpret_cast<volatile int *>(&sm.dead)) return false;
   const float2 enter = sm.enter[half][lane];
   if (tells) {
     const float2 leave = gs_through(map, enter);
-    record_put(p.states + (int64_t)tile * 32 + lane, leave);
+    record_put(p.states + at, leave);
     if (q.step == 0)  // known whole: nothing before it counts
-      record_put(p.maps + (int64_t)tile * 32 + lane,
-                 make_float4(-0.0f, -0.0f, leave.x, leave.y));
+      record_put(p.maps + at, make_float4(-0.0f, -0.0f, leave.x, leave.y));
   }
   *h = gs_through(pre, enter);
   return true;
@@ -182,7 +187,7 @@ __device__ __forceinline__ bool exchange(S &sm, const Scan &p, const Tile &q, in
 // enter them.  REVERSE: the steps go from the rows' last tokens to the first.
 template <typename S, bool PACKED, bool REVERSE>
 __device__ __forceinline__ void look_up(S &sm, const Maps &in, const Scan &p) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, l = lane % kLanes;  // (both halves read the same records)
   const int per_step = p.rows * p.nblk;
   // one lane: tile t's copies, into stage s
   auto fetch = [&](int s, int t) {
@@ -223,13 +228,13 @@ __device__ __forceinline__ void look_up(S &sm, const Maps &in, const Scan &p) {
     if (q.left <= 0) return;  // so is every later tile's: no copy is under way
     int next = 0;
     if (lane == 0) next = (int)atomicAdd(p.ticket, 1u);  // wanted when the segments are there
-    const int d = q.cb * kWidth + 2 * lane;
+    const int d = q.cb * kWidth + 2 * l;
     const int tile = q.step * per_step + q.row * p.nblk + q.cb;
     const int between = min(q.step, p.back - 1);
     bool fetched = false, entered = false, based = q.step < p.back;
     int folded = 0;  // maps, of those between
-    const float2 *base = p.states + ((int64_t)tile - (int64_t)p.back * per_step) * 32 + lane;
-    const float4 *maps = p.maps + ((int64_t)tile - (int64_t)between * per_step) * 32 + lane;
+    const float2 *base = p.states + ((int64_t)tile - (int64_t)p.back * per_step) * kLanes + l;
+    const float4 *maps = p.maps + ((int64_t)tile - (int64_t)between * per_step) * kLanes + l;
     float2 h = make_float2(0.0f, 0.0f);
     if (!PACKED && q.step == 0 && p.first != nullptr && d < p.D)
       h = *reinterpret_cast<const float2 *>(p.first + (int64_t)q.row * p.D + d);
@@ -241,7 +246,7 @@ __device__ __forceinline__ void look_up(S &sm, const Maps &in, const Scan &p) {
         if (!based) b = record_get(base);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-          if (folded + k < between) m[k] = record_get(maps + (int64_t)(folded + k) * per_step * 32);
+          if (folded + k < between) m[k] = record_get(maps + (int64_t)(folded + k) * per_step * kLanes);
         unsigned int there = based || is_set(b) ? 1u << 31 : 0u;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
@@ -258,7 +263,7 @@ __device__ __forceinline__ void look_up(S &sm, const Maps &in, const Scan &p) {
           entered = folded == between;
         }
         if (entered) {
-          sm.enter[half][lane] = h;
+          sm.enter[half][l] = h;
           entered_signal(half);
         }
       }
@@ -298,9 +303,9 @@ inline Plan plan_of(int64_t rows, int64_t L, int D, int tile_tokens, bool packed
   p.nblk = (int)ceil_div(D, kWidth);
   p.steps = (int)ceil_div(L, tile_tokens);
   p.tiles = rows * p.steps * p.nblk;
-  const size_t records = p.steps > 1 ? (size_t)p.tiles * 32 : 0;
+  const size_t records = p.steps > 1 ? (size_t)align_up(p.tiles, 2) * kLanes : 0;
   p.ncs = 256;  // after the counter and the flag of wrong offsets
-  p.maps = p.ncs + align_up((size_t)p.nblk * kWidth * 4, 256);
+  p.maps = p.ncs + align_up((size_t)D * 4, 256);
   p.states = p.maps + records * 16;
   p.marks = p.states + records * 8;
   p.total = p.marks + (packed ? align_up((size_t)L * 4, 256) : 0);
