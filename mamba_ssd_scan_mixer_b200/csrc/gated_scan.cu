@@ -37,6 +37,17 @@ __device__ __forceinline__ float4 make_maps(const unsigned char *in, const int *
                                             int d, F2 (&a)[S::kTokens], F2 (&b)[S::kTokens]) {
   using T = typename S::T;
   F2 A = f2(1.0f), H = f2(0.0f);
+  // the state of the first sequence that begins here: under way during the arithmetic
+  // before it (one sequence's begin is the usual case)
+  auto state_of = [&](int i) {
+    float2 h = make_float2(0.0f, 0.0f);
+    if (p.first != nullptr && d < p.D)
+      h = *reinterpret_cast<const float2 *>(p.first + (int64_t)(marks[i] >> 2) * p.D + d);
+    return f2(h.x, h.y);
+  };
+  const int one = RESETS ? __ffs(begins) - 1 : -1;
+  F2 state = f2(0.0f);
+  if (RESETS && one >= 0) state = state_of(one);
 #pragma unroll
   for (int i = 0; i < S::kTokens; ++i) {
     const unsigned char *row = in + i * S::kRow;
@@ -50,11 +61,7 @@ __device__ __forceinline__ float4 make_maps(const unsigned char *in, const int *
       b[i] = f2(0.0f);
     }
     if (RESETS && (begins >> i & 1)) {
-      if (p.first != nullptr && d < p.D) {
-        const float2 h =
-            *reinterpret_cast<const float2 *>(p.first + (int64_t)(marks[i] >> 2) * p.D + d);
-        b[i] = fma2(a[i], f2(h.x, h.y), b[i]);
-      }
+      b[i] = fma2(a[i], i == one ? state : state_of(i), b[i]);
       A = f2(-0.0f);
       H = b[i];
     } else {
@@ -114,13 +121,17 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
     }
     const F2 k = f2(ncs.x, ncs.y);
     float4 map;
-    if (__all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f) && whole)
+    const bool close = __all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f);
+    if (close && whole)
       map = n == S::kTile
                 ? make_maps<S, true, false, true>(in, marks, 0, k, n - first, p, d, a, b)
                 : make_maps<S, false, false, true>(in, marks, 0, k, n - first, p, d, a, b);
+    else if (PACKED && close)
+      map = make_maps<S, false, PACKED, true>(in, marks, begins, k, n - first, p, d, a, b);
     else
       map = make_maps<S, false, PACKED, false>(in, marks, begins, k, n - first, p, d, a, b);
     sm.seg[half][seg][lane] = map;
+    if (PACKED && threadIdx.x % 32 == 0) sm.resets[half][warp] = !whole;
     typename Pair<T>::V gate[GATED ? S::kTokens : 1];
     if (GATED) {
 #pragma unroll

@@ -41,6 +41,16 @@ __device__ __forceinline__ float4 back_map(const unsigned char *in, const int *m
                                            int D, int d) {
   using T = typename S::T;
   F2 A = f2(1.0f), E = f2(0.0f);
+  // the final gradient of the last sequence that ends here: under way early
+  auto gradient_of = [&](int i) {
+    float2 v = make_float2(0.0f, 0.0f);
+    if (dh != nullptr && d < D)
+      v = *reinterpret_cast<const float2 *>(dh + (int64_t)(marks[i] >> 2) * D + d);
+    return f2(v.x, v.y);
+  };
+  const int one = RESETS ? 31 - __clz(lasts) : -1;
+  F2 gradient = f2(0.0f);
+  if (RESETS && one >= 0) gradient = gradient_of(one);
 #pragma unroll
   for (int i = kGsChunk - 1; i >= 0; --i) {
     if (!FULL && i >= n) continue;
@@ -49,10 +59,7 @@ __device__ __forceinline__ float4 back_map(const unsigned char *in, const int *m
     decay2<NEAR>(mul2(ncs, sigmoid2(gs_pair<T>(row))), &a, &less);
     if (GATED) dy = mul2(dy, silu2(gs_pair<T>(row + 2 * S::kTensor)));
     if (RESETS && (lasts >> i & 1)) {
-      if (dh != nullptr && d < D) {
-        const float2 v = *reinterpret_cast<const float2 *>(dh + (int64_t)(marks[i] >> 2) * D + d);
-        dy = add2(dy, f2(v.x, v.y));
-      }
+      dy = add2(dy, i == one ? gradient : gradient_of(i));
       A = f2(-0.0f);
       E = mul2(a, dy);
     } else {
@@ -91,7 +98,8 @@ __global__ void __launch_bounds__(kThreads, (kCarryResident<GATED>))
     const F2 k = f2(ncs.x, ncs.y);
     constexpr int kChunks = S::kTokens / kGsChunk;  // of a thread
     float4 maps_of[kChunks], map;
-    const bool close = __all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f) && n == S::kTile;
+    bool resets = false;
+    const bool close = __all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f);
 #pragma unroll
     for (int c = kChunks - 1; c >= 0; --c) {
       const int at = first + c * kGsChunk;
@@ -101,14 +109,18 @@ __global__ void __launch_bounds__(kThreads, (kCarryResident<GATED>))
       if (PACKED)
         lasts = __ballot_sync(0xffffffffu, lane < min(kGsChunk, n - at) && (marks[lane] & kLast));
       const bool whole = lasts == 0;  // (no sequence ends in either half)
+      resets |= !whole;
       lasts = lasts >> (threadIdx.x & 16) & 0xffff;
-      maps_of[c] = close && whole
-                       ? back_map<S, true, false, true, GATED>(in, marks, 0, k, n - at, dh, p.D, d)
-                       : back_map<S, false, PACKED, false, GATED>(in, marks, lasts, k, n - at, dh,
-                                                                  p.D, d);
+      if (close && whole && n == S::kTile)
+        maps_of[c] = back_map<S, true, false, true, GATED>(in, marks, 0, k, n - at, dh, p.D, d);
+      else if (close)
+        maps_of[c] = back_map<S, false, PACKED, true, GATED>(in, marks, lasts, k, n - at, dh, p.D, d);
+      else
+        maps_of[c] = back_map<S, false, PACKED, false, GATED>(in, marks, lasts, k, n - at, dh, p.D, d);
       map = c == kChunks - 1 ? maps_of[c] : gs_then(map, maps_of[c]);
     }
     sm.seg[half][seg][lane] = map;
+    if (PACKED && threadIdx.x % 32 == 0) sm.resets[half][threadIdx.x / 32] = resets;
     __syncwarp();
     if (threadIdx.x % 32 == 0) mbar_arrive(&sm.segs[half]);
     float2 e;

@@ -54,6 +54,7 @@ struct Tile {
 
 template <typename T_, int TENSORS, int TOKENS> struct Shared {
   using T = T_;
+  static_assert(kWarps == 4, "resets");
   static constexpr int kTensors = TENSORS, kTile = TOKENS, kStages = 2;
   static constexpr int kTokens = TOKENS / kSegs;        // of a thread
   static constexpr int kRow = kWidth * (int)sizeof(T);  // bytes of a token
@@ -63,6 +64,7 @@ template <typename T_, int TENSORS, int TOKENS> struct Shared {
   alignas(16) float ncs[kStages][kWidth];
   float4 seg[2][kSegs][kLanes];
   float2 enter[2][kLanes];
+  alignas(16) int resets[2][kWarps];  // packed rows: a sequence begins among the warp's tokens
   uint64_t full[kStages], segs[2];
   Tile tile[kStages];
   int dead;  // a wait ran out: everybody leaves after the next `entered`
@@ -140,9 +142,12 @@ template <typename S, bool PACKED> __device__ __forceinline__ bool begin(S &sm, 
 template <bool PACKED, typename S>
 __device__ __forceinline__ float4 compose_before(const S &sm, int half, int seg, int lane) {
   if (PACKED) {
-    float4 pre = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-    for (int k = 0; k < seg; ++k) pre = gs_then(pre, sm.seg[half][k][lane]);
-    return pre;
+    const int4 r = *reinterpret_cast<const int4 *>(sm.resets[half]);
+    if (r.x | r.y | r.z | r.w) {
+      float4 pre = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+      for (int k = 0; k < seg; ++k) pre = gs_then(pre, sm.seg[half][k][lane]);
+      return pre;
+    }
   }
   F2 A = f2(1.0f), H = f2(0.0f);
 #pragma unroll
