@@ -797,6 +797,7 @@ MAMBA2_API int mamba2_gated_scan_step(const mamba2_gated_scan_dims *dims, const 
   if (dims == nullptr) return MAMBA2_ERR_INVALID_ARG;
   d = *dims;
   d.seqlen = 1;
+  if (d.batch > (int64_t)65535 * 8) return MAMBA2_ERR_UNSUPPORTED;  // grid limit
   const int st = gated_scan_inputs(&d, lam, x, x_row_stride, r, r_row_stride, g, g_row_stride, z,
                                    z_row_stride, d.batch > 0, &a);
   if (st != MAMBA2_OK) return st;

@@ -29,25 +29,12 @@ template <bool GATED> constexpr int kResident = GATED ? 3 : 4;
 template <typename T, bool GATED>
 using Tiles = Shared<T, GATED ? 4 : 3, sizeof(T) == 2 ? 128 : 64>;
 
-// Step 2: a and b of the thread's tokens, and their composition.  `begins`: the tokens (a
-// bit each) that begin a sequence of packed rows.
-template <typename S, bool FULL, bool RESETS, bool NEAR>
-__device__ __forceinline__ float4 make_maps(const unsigned char *in, const int *marks,
-                                            unsigned int begins, F2 ncs, int n, const Scan &p,
-                                            int d, F2 (&a)[S::kTokens], F2 (&b)[S::kTokens]) {
+// Step 2: a and b of the thread's tokens, and their composition.
+template <typename S, bool FULL, bool NEAR>
+__device__ __forceinline__ float4 make_maps(const unsigned char *in, F2 ncs, int n,
+                                            F2 (&a)[S::kTokens], F2 (&b)[S::kTokens]) {
   using T = typename S::T;
   F2 A = f2(1.0f), H = f2(0.0f);
-  // the state of the first sequence that begins here: under way during the arithmetic
-  // before it (one sequence's begin is the usual case)
-  auto state_of = [&](int i) {
-    float2 h = make_float2(0.0f, 0.0f);
-    if (p.first != nullptr && d < p.D)
-      h = *reinterpret_cast<const float2 *>(p.first + (int64_t)(marks[i] >> 2) * p.D + d);
-    return f2(h.x, h.y);
-  };
-  const int one = RESETS ? __ffs(begins) - 1 : -1;
-  F2 state = f2(0.0f);
-  if (RESETS && one >= 0) state = state_of(one);
 #pragma unroll
   for (int i = 0; i < S::kTokens; ++i) {
     const unsigned char *row = in + i * S::kRow;
@@ -60,17 +47,38 @@ __device__ __forceinline__ float4 make_maps(const unsigned char *in, const int *
       a[i] = f2(1.0f);
       b[i] = f2(0.0f);
     }
-    if (RESETS && (begins >> i & 1)) {
-      b[i] = fma2(a[i], i == one ? state : state_of(i), b[i]);
-      A = f2(-0.0f);
-      H = b[i];
-    } else {
-      A = mul2(A, a[i]);
-      H = fma2(a[i], H, b[i]);
-    }
+    A = mul2(A, a[i]);
+    H = fma2(a[i], H, b[i]);
   }
   const float2 x = unpack(A), y = unpack(H);
   return make_float4(x.x, x.y, y.x, y.y);
+}
+
+// Packed rows: where a sequence begins (a bit of `begins`) its state comes in, and nothing
+// from before.  Apart from the arithmetic above, so that this seldom used code is short:
+// a second copy of all of it, fetched anew at each sequence, held the whole row up by 2 us.
+template <typename S>
+__device__ __forceinline__ float4 reset_maps(const int *marks, unsigned int begins, const Scan &p,
+                                             int d, F2 (&a)[S::kTokens], F2 (&b)[S::kTokens]) {
+  for (unsigned int left = begins; left != 0; left &= left - 1) {
+    const int one = __ffs(left) - 1;
+    float2 h = make_float2(0.0f, 0.0f);
+    if (p.first != nullptr && d < p.D)
+      h = *reinterpret_cast<const float2 *>(p.first + (int64_t)(marks[one] >> 2) * p.D + d);
+#pragma unroll
+    for (int i = 0; i < S::kTokens; ++i)
+      if (i == one) {
+        b[i] = fma2(a[i], f2(h.x, h.y), b[i]);
+        a[i] = f2(-0.0f);
+      }
+  }
+  float4 map = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < S::kTokens; ++i) {
+    const float2 x = unpack(a[i]), y = unpack(b[i]);
+    map = gs_then(map, make_float4(x.x, x.y, y.x, y.y));
+  }
+  return map;
 }
 
 __device__ __forceinline__ void store_pair(float *p, float2 v) {
@@ -111,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
     // packed rows: which of the warp's tokens begin and end a sequence
     unsigned int begins = 0, ends = 0;
     bool whole = true;  // (no sequence begins in either half)
+    int owner = 0;      // of the first of the ends
     if (PACKED) {
       const int mark = lane < min(S::kTokens, n - first) ? marks[lane] : 0, up = threadIdx.x & 16;
       begins = __ballot_sync(0xffffffffu, mark & kFirst);
@@ -118,18 +127,14 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
       whole = begins == 0;
       begins = begins >> up & 0xffff;
       ends = ends >> up & 0xffff;
+      if (ends != 0) owner = marks[__ffs(ends) - 1] >> 2;
     }
     const F2 k = f2(ncs.x, ncs.y);
     float4 map;
     const bool close = __all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f);
-    if (close && whole)
-      map = n == S::kTile
-                ? make_maps<S, true, false, true>(in, marks, 0, k, n - first, p, d, a, b)
-                : make_maps<S, false, false, true>(in, marks, 0, k, n - first, p, d, a, b);
-    else if (PACKED && close)
-      map = make_maps<S, false, PACKED, true>(in, marks, begins, k, n - first, p, d, a, b);
-    else
-      map = make_maps<S, false, PACKED, false>(in, marks, begins, k, n - first, p, d, a, b);
+    if (close && n == S::kTile) map = make_maps<S, true, true>(in, k, n - first, a, b);
+    else map = make_maps<S, false, false>(in, k, n - first, a, b);
+    if (PACKED && !whole) map = reset_maps<S>(marks, begins, p, d, a, b);
     sm.seg[half][seg][lane] = map;
     if (PACKED && threadIdx.x % 32 == 0) sm.resets[half][warp] = !whole;
     typename Pair<T>::V gate[GATED ? S::kTokens : 1];
@@ -150,30 +155,32 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
     F2 hh = f2(h.x, h.y);
     if (y_out != nullptr) {
       T *y = y_out + token * p.D + d;
-      auto run = [&](auto all) {  // all: every token of every lane is stored, no sequence's end
+      // all: every token of every lane is stored, and no sequence begins or ends
+      auto run = [&](auto all) {
 #pragma unroll
         for (int i = 0; i < S::kTokens; ++i) {
-          if (!decltype(all)::value && PACKED && (begins >> i & 1)) hh = b[i];
+          if (PACKED && !decltype(all)::value && (begins >> i & 1)) hh = b[i];
           else hh = fma2(a[i], hh, b[i]);
           F2 o = hh;
           if (GATED) {
             const float2 z = Pair<T>::get(gate[i]);
             o = mul2(hh, mul2(f2(z.x, z.y), sigmoid2(f2(z.x, z.y))));
           }
-          if (decltype(all)::value) {
+          if (decltype(all)::value || (real && i < n - first)) {
             store_pair(y, unpack(o));
-          } else if (real && i < n - first) {
-            store_pair(y, unpack(o));
-            if (PACKED && (ends >> i & 1))
-              *reinterpret_cast<float2 *>(
-                  h_out + (int64_t)(p.marks[t0 + first + i] >> 2) * p.D + d) = unpack(hh);
+            if (PACKED && !decltype(all)::value && (ends >> i & 1)) {
+              // (a short sequence's mark is read again: the stage may hold another tile)
+              const int who = (ends & ((1u << i) - 1)) == 0 ? owner : p.marks[t0 + first + i] >> 2;
+              *reinterpret_cast<float2 *>(h_out + (int64_t)who * p.D + d) = unpack(hh);
+            }
           }
           y += p.D;
         }
       };
       if (__all_sync(0xffffffffu, real && n - first >= S::kTokens && (begins | ends) == 0))
         run(std::true_type());
-      else run(std::false_type());
+      else
+        run(std::false_type());
     }
     if (!PACKED && h_out != nullptr && q.step == p.steps - 1 && real && first < n &&
         n <= first + S::kTokens)
@@ -182,33 +189,77 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
   }
 }
 
+// ---------------------------------------------------------------- decode
 template <typename T> struct In {
   const T *x, *r, *g, *z;
   int64_t ld_x, ld_r, ld_g, ld_z;
 };
 
-template <typename T>
-__global__ void gs_step_kernel(In<T> in, const float *lam, float c, int64_t n2, int D, float *h,
-                               T *y) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= n2) return;
-  const int64_t b = i / (D / 2);
-  const int d = 2 * (int)(i % (D / 2));
-  const float2 x = ld2(in.x + b * in.ld_x + d), r = ld2(in.r + b * in.ld_r + d),
-               g = ld2(in.g + b * in.ld_g + d);
-  const Gate p = gs_gate(r.x, g.x, -c * softplus_f(lam[d])),
-             q = gs_gate(r.y, g.y, -c * softplus_f(lam[d + 1]));
-  float2 *hp = reinterpret_cast<float2 *>(h + b * D + d);
-  float2 v = *hp;
-  v.x = p.a * v.x + p.m * p.G * x.x;
-  v.y = q.a * v.y + q.m * q.G * x.y;
-  *hp = v;
-  if (in.z != nullptr) {
-    const float2 z = ld2(in.z + b * in.ld_z + d);
-    v.x *= z.x * gs_sigmoid(z.x);
-    v.y *= z.y * gs_sigmoid(z.y);
+// 16 bytes of a row: V = 4 or 8 channels.
+template <typename T> struct Lane {
+  static constexpr int V = 16 / (int)sizeof(T);
+  uint4 w;
+  __device__ __forceinline__ void load(const T *p) { w = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ const void *pair(int k) const {
+    return reinterpret_cast<const T *>(&w) + 2 * k;
   }
-  st2(y + b * D + d, v.x, v.y);
+};
+
+// One token of every sequence.  Bound by the state's and the rows' bytes (and, for few
+// sequences, by the launch): a thread takes 16 bytes of each row, two rows one after the
+// other; the decays' factors are made once for a block's rows.
+constexpr int kStepGroups = 64, kStepRows = 4, kStepTurns = 2;
+template <typename T, bool GATED>
+__global__ void __launch_bounds__(kStepGroups *kStepRows)
+    gs_step_kernel(In<T> in, const float *__restrict__ lam, float c, int64_t batch, int D,
+                   float *__restrict__ h, T *__restrict__ y) {
+  constexpr int V = Lane<T>::V;
+  __shared__ float ncs[kStepGroups * V];
+  const int group = threadIdx.x % kStepGroups, c0 = blockIdx.x * kStepGroups * V;
+  const int d = c0 + group * V;
+  const int64_t row = (int64_t)blockIdx.y * (kStepRows * kStepTurns) + threadIdx.x / kStepGroups;
+  Lane<T> x[kStepTurns], r[kStepTurns], g[kStepTurns], z[kStepTurns];
+  float4 s[kStepTurns][V / 4];
+#pragma unroll
+  for (int k = 0; k < kStepTurns; ++k) {
+    const int64_t b = row + k * kStepRows;
+    if (b < batch && d < D) {
+      x[k].load(in.x + b * in.ld_x + d);
+      r[k].load(in.r + b * in.ld_r + d);
+      g[k].load(in.g + b * in.ld_g + d);
+      if (GATED) z[k].load(in.z + b * in.ld_z + d);
+#pragma unroll
+      for (int j = 0; j < V / 4; ++j) s[k][j] = *reinterpret_cast<const float4 *>(h + b * D + d + 4 * j);
+    }
+  }
+  for (int i = threadIdx.x; i < kStepGroups * V; i += kStepGroups * kStepRows)
+    ncs[i] = c0 + i < D ? -c * softplus_f(lam[c0 + i]) * kLog2e : 0.0f;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kStepTurns; ++k) {
+    const int64_t b = row + k * kStepRows;
+    if (b >= batch || d >= D) continue;
+    float *state = reinterpret_cast<float *>(s[k]);
+    uint4 out;
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+      const float2 n = *reinterpret_cast<const float2 *>(&ncs[group * V + 2 * j]);
+      const Coeffs q = coefficients<false>(gs_pair<T>(x[k].pair(j)), gs_clamped<T>(r[k].pair(j)),
+                                           gs_clamped<T>(g[k].pair(j)), f2(n.x, n.y));
+      F2 v = fma2(q.a, f2(state[2 * j], state[2 * j + 1]), q.b);
+      const float2 w = unpack(v);
+      state[2 * j] = w.x;
+      state[2 * j + 1] = w.y;
+      if (GATED) {
+        const F2 zz = gs_pair<T>(z[k].pair(j));
+        v = mul2(v, mul2(zz, sigmoid2(zz)));
+      }
+      st2(reinterpret_cast<T *>(&out) + 2 * j, unpack(v));
+    }
+    *reinterpret_cast<uint4 *>(y + b * D + d) = out;
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) *reinterpret_cast<float4 *>(h + b * D + d + 4 * j) = s[k][j];
+  }
 }
 
 template <typename T> In<T> inputs(const GatedScanArgs &a) {
@@ -251,9 +302,11 @@ template <typename T> cudaError_t prefill(const GatedScanArgs &a) {
 }
 
 template <typename T> cudaError_t step(const GatedScanArgs &a) {
-  const int64_t n2 = a.batch * (a.D / 2);
-  gs_step_kernel<T><<<(unsigned)ceil_div(n2, 128), 128, 0, a.stream>>>(
-      inputs<T>(a), a.lam, a.c, n2, a.D, a.h, static_cast<T *>(a.y));
+  const dim3 grid((unsigned)ceil_div(a.D, kStepGroups * Lane<T>::V),
+                  (unsigned)ceil_div(a.batch, kStepRows * kStepTurns));
+  const auto kernel = a.z != nullptr ? gs_step_kernel<T, true> : gs_step_kernel<T, false>;
+  kernel<<<grid, kStepGroups * kStepRows, 0, a.stream>>>(inputs<T>(a), a.lam, a.c, a.batch, a.D,
+                                                         a.h, static_cast<T *>(a.y));
   return cudaGetLastError();
 }
 

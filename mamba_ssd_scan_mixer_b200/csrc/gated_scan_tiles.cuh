@@ -76,7 +76,7 @@ template <typename T_, int TENSORS, int TOKENS> struct Shared {
 __global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, uint4 *records,
                                int64_t nrecords, unsigned int *ticket, const int32_t *cu, int64_t batch,
                                int64_t L, int *marks, unsigned int *bad,
-                               const float *empty_in, float *empty_out) {
+                               const float *first, const float *empty_in, float *empty_out) {
   launch_dependents();
   const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t all = (int64_t)gridDim.x * blockDim.x;
@@ -96,6 +96,12 @@ __global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, uin
     if (wrong) atomicOr(&g_gs_errors, kErrSeqlens);
   }
   if (wrong) return;
+  // the sequences' states into L2: each is wanted at once when its first token comes up,
+  // and tiles of the whole row wait for it (2 us a sequence without this)
+  constexpr int64_t kMostPrefetched = 32 << 20;
+  if (first != nullptr && batch * D * 4 <= kMostPrefetched)
+    for (int64_t i = at * 32; i < batch * D; i += all * 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(first + i));
   for (int64_t t = at; t < L; t += all) {
     int64_t lo = 0, hi = batch - 1;  // the sequence of token t: the first that ends after it
     while (lo < hi) {
@@ -145,7 +151,9 @@ __device__ __forceinline__ float4 compose_before(const S &sm, int half, int seg,
     const int4 r = *reinterpret_cast<const int4 *>(sm.resets[half]);
     if (r.x | r.y | r.z | r.w) {
       float4 pre = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-      for (int k = 0; k < seg; ++k) pre = gs_then(pre, sm.seg[half][k][lane]);
+#pragma unroll
+      for (int k = 0; k < kSegs - 1; ++k)
+        if (k < seg) pre = gs_then(pre, sm.seg[half][k][lane]);
       return pre;
     }
   }
@@ -341,7 +349,7 @@ inline cudaError_t prepare(const GatedScanArgs &a, const Plan &w, char *ws, cons
   gs_prep_kernel<<<(unsigned)std::min<int64_t>(ceil_div(work, 256), 148 * 4), 256, 0, a.stream>>>(
       a.lam, a.c, a.D, const_cast<float *>(p->ncs), reinterpret_cast<uint4 *>(ws + w.maps),
       nrecords, p->ticket, a.cu, a.batch, a.L, const_cast<int *>(p->marks),
-      const_cast<unsigned int *>(p->bad), empty_in, empty_out);
+      const_cast<unsigned int *>(p->bad), first, empty_in, empty_out);
   return cudaGetLastError();
 }
 
