@@ -158,6 +158,27 @@ constexpr int kApplyThreads = 32 * kWarps;
 template <typename T, bool GATED>
 constexpr int kApplyResident = GATED ? 2 : 3;
 
+// The tiles of a block, `stride` apart, without a division each.
+struct Walk {
+  int cb, row, step, dcb, drow, dstep;
+  __device__ __forceinline__ Walk(int tile, int stride, const Scan &p)
+      : cb(tile % p.nblk), row(tile / p.nblk % p.rows), step(tile / p.nblk / p.rows),
+        dcb(stride % p.nblk), drow(stride / p.nblk % p.rows), dstep(stride / p.nblk / p.rows) {}
+  __device__ __forceinline__ void next(const Scan &p) {
+    cb += dcb;
+    row += drow;
+    step += dstep;
+    if (cb >= p.nblk) {
+      cb -= p.nblk;
+      ++row;
+    }
+    if (row >= p.rows) {
+      row -= p.rows;
+      ++step;
+    }
+  }
+};
+
 template <typename T> struct Apply {
   Scan p;  // (steps, nblk and tiles: of kApplyTile tokens and kApplyWidth channels)
   const float *ck, *carry;  // [rows][chunks][D]
@@ -186,8 +207,8 @@ template <> __device__ __forceinline__ F2 get_state<float>(const unsigned char *
   return f2(v.x, v.y);
 }
 
-// One warp's 16 tokens.  FAST: all of them there, no sequence begins or ends among them,
-// and decays near one.
+// One warp's 16 tokens.  FAST: all of them and of the channels there, no sequence begins or
+// ends among them, and decays near one.
 template <typename T, bool GATED, bool PACKED, bool FAST>
 __device__ __forceinline__ F2 apply_tokens(ApplyShared<T, GATED> &sm, int s,
                                            const Apply<T> &q, int row, int64_t t0, int n, int first,
@@ -203,7 +224,7 @@ __device__ __forceinline__ F2 apply_tokens(ApplyShared<T, GATED> &sm, int s,
   const float2 h0 = *reinterpret_cast<const float2 *>(&sm.h[s][warp][2 * lane]);
   const float2 e0 = *reinterpret_cast<const float2 *>(&sm.e[s][warp][2 * lane]);
   F2 h = f2(h0.x, h0.y), e = f2(e0.x, e0.y), dl = f2(0.0f);
-  const bool real = d < p.D;
+  const bool real = FAST || d < p.D;
   const int count = FAST ? K : min(K, n - first);
   F2 R[K], G[K];
 #pragma unroll
@@ -229,13 +250,16 @@ __device__ __forceinline__ F2 apply_tokens(ApplyShared<T, GATED> &sm, int s,
   // is zero.)
   const F2 ncs2 = F2{ncs.v ^ q.zero};
   in += q.zero;
-  // the same for every lane, and 32-bit offsets from there
-  const int64_t tile0 = ((int64_t)row * p.L + t0) * p.D + (d - 2 * lane);
-  T *const dx_out = q.dx + tile0, *const dr_out = q.dr + tile0, *const dg_out = q.dg + tile0;
-  T *const dz_out = GATED ? q.dz + tile0 : nullptr;
-  const uint32_t off0 = (uint32_t)first * p.D + 2 * lane;
+  const int64_t behind = ((int64_t)row * p.L + t0 + first + K) * p.D + d;
+  T *dx_out = q.dx + behind, *dr_out = q.dr + behind, *dg_out = q.dg + behind,
+    *dz_out = GATED ? q.dz + behind : nullptr;
+  const int64_t stride = p.D;
 #pragma unroll
   for (int i = K - 1; i >= 0; --i) {
+    dx_out -= stride;
+    dr_out -= stride;
+    dg_out -= stride;
+    if (GATED) dz_out -= stride;
     if (!FAST && i >= count) continue;
     const unsigned char *at = in + i * S::kRow;
     const F2 x = gs_pair<T>(at);
@@ -253,7 +277,7 @@ __device__ __forceinline__ F2 apply_tokens(ApplyShared<T, GATED> &sm, int s,
       const F2 ht = fma2(a, before, b);
       // silu' = sig (1 + z (1 - sig))
       const F2 slope = mul2(sig, fma2(z, fma2(sig, f2(-1.0f), f2(1.0f)), f2(1.0f)));
-      if (real) st2(dz_out + (off0 + i * p.D), unpack(mul2(mul2(dy, ht), slope)));
+      if (real) st2(dz_out, unpack(mul2(mul2(dy, ht), slope)));
       dy = mul2(dy, mul2(z, sig));
     }
     if (!FAST && PACKED && (marks[i] & kLast)) {
@@ -275,10 +299,9 @@ __device__ __forceinline__ F2 apply_tokens(ApplyShared<T, GATED> &sm, int s,
     const F2 dr = mul2(dla, mul2(mul2_flush(t, f2(0.6931471805599453f * down2)),
                                  fma2(R[i], f2(-up2), f2(up2))));
     if (real) {
-      const uint32_t o = off0 + i * p.D;
-      st2(dx_out + o, unpack(dx));
-      st2(dr_out + o, unpack(dr));
-      st2(dg_out + o, unpack(dg));
+      st2(dx_out, unpack(dx));
+      st2(dr_out, unpack(dr));
+      st2(dg_out, unpack(dg));
     }
     if (!FAST && PACKED && (marks[i] & kFirst) && q.dh_in != nullptr && real)
       *reinterpret_cast<float2 *>(q.dh_in + (int64_t)(marks[i] >> 2) * p.D + d) = unpack(e);
@@ -308,10 +331,9 @@ __global__ void __launch_bounds__(kApplyThreads, (kApplyResident<T, GATED>))
   if (PACKED && *p.bad) return;
   const int64_t nch = (p.L + kGsChunk - 1) / kGsChunk;
   // one thread: a tile's copies, into stage s
-  auto fetch = [&](int s, int tile) {
-    if (tile >= p.tiles) return;
-    const int cb = tile % p.nblk, row = tile / p.nblk % p.rows;
-    const int t0 = tile / p.nblk / p.rows * kApplyTile;
+  auto fetch = [&](int s, const Walk &w) {
+    if (w.step >= p.steps) return;
+    const int cb = w.cb, row = w.row, t0 = w.step * kApplyTile;
     const int n = (int)min((int64_t)kApplyTile, p.L - t0), chunks = (n + kGsChunk - 1) / kGsChunk;
     const uint32_t wide = (uint32_t)min(kApplyWidth, p.D - cb * kApplyWidth) * 4;
     const uint32_t mark_bytes = PACKED ? (n * 4 + 15) / 16 * 16 : 0;
@@ -329,21 +351,21 @@ __global__ void __launch_bounds__(kApplyThreads, (kApplyResident<T, GATED>))
     if (PACKED) bulk_g2s(sm.marks[s], p.marks + t0, mark_bytes, &sm.full[s]);
   };
   constexpr int kFetcher = 32 * kWarps - 1;
+  Walk at(blockIdx.x, gridDim.x, p), ahead = at;
   if (threadIdx.x == kFetcher)
-    for (int s = 0; s < S::kStages; ++s) fetch(s, blockIdx.x + s * gridDim.x);
+    for (int s = 0; s < S::kStages; ++s, ahead.next(p)) fetch(s, ahead);
   const int first = warp * kGsChunk;
-  int it = 0;
-  for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, ++it) {
+  for (int it = 0; at.step < p.steps; ++it, at.next(p)) {
     const int s = it % S::kStages, half = it & 1;
     const bool there = mbar_wait_parked(&sm.full[s], (it / S::kStages) & 1, &g_gs_errors);
     if (!there) sm.dead = 1;
-    const int cb = tile % p.nblk, row = tile / p.nblk % p.rows, step = tile / p.nblk / p.rows;
+    const int cb = at.cb, row = at.row, step = at.step;
     const int t0 = step * kApplyTile, n = (int)min((int64_t)kApplyTile, p.L - t0);
     const int d = cb * kApplyWidth + 2 * lane;
     F2 dl = f2(0.0f);
     if (there && first < n) {
       const float2 nn = *reinterpret_cast<const float2 *>(&sm.ncs[s][2 * lane]);
-      bool fast = fminf(nn.x, nn.y) >= -0.5f && n - first >= kGsChunk;
+      bool fast = fminf(nn.x, nn.y) >= -0.5f && n - first >= kGsChunk && d < p.D;
       if (PACKED) fast = fast && !(lane < kGsChunk && (sm.marks[s][first + lane % kGsChunk] & 3));
       if (__all_sync(0xffffffffu, fast))
         dl = apply_tokens<T, GATED, PACKED, true>(sm, s, q, row, t0, n, first, lane, d);
@@ -356,11 +378,14 @@ __global__ void __launch_bounds__(kApplyThreads, (kApplyResident<T, GATED>))
     if (*reinterpret_cast<volatile int *>(&sm.dead)) {
       // what this block has under way lands before it leaves
       if (threadIdx.x == kFetcher)
-        for (int i = it; i < it + S::kStages && tile + (i - it) * (int)gridDim.x < p.tiles; ++i)
+        for (int i = it; i < it + S::kStages && at.step < p.steps; ++i, at.next(p))
           mbar_wait_parked(&sm.full[i % S::kStages], (i / S::kStages) & 1, &g_gs_errors);
       return;
     }
-    if (threadIdx.x == kFetcher) fetch(s, tile + S::kStages * (int)gridDim.x);
+    if (threadIdx.x == kFetcher) {
+      fetch(s, ahead);
+      ahead.next(p);
+    }
     if (warp == 0) {  // (the next tile's sums go to the other half)
       float2 v = sm.dl[half][0][lane];
 #pragma unroll
