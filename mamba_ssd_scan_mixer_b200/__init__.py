@@ -470,7 +470,7 @@ def gated_scan_checkpoints(dims: Mamba2GatedScanDims, packed: bool = False, devi
 
 
 def _need(t, name, shape, dtype, device, contiguous=True):
-    if t.device != device or t.dtype != dtype or t.shape != shape:
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name}: {tuple(shape)} {dtype} on {device} expected, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
     if contiguous and not t.is_contiguous():
@@ -479,61 +479,64 @@ def _need(t, name, shape, dtype, device, contiguous=True):
 
 def _row_stride(t, name):
     """Elements from one token to the next of [..., tokens, D] rows that follow one another."""
-    st = t.stride()
+    st, shape = t.stride(), t.shape
     if st[-1] != 1:
         raise ValueError(f"{name}: last dimension must be contiguous")
-    if t.dim() == 2:
-        return st[0] if t.shape[0] > 1 else max(st[0], t.shape[1])
-    b, n = t.shape[0], t.shape[1]
-    rs = st[1] if n > 1 else (st[0] if b > 1 else max(st[1], t.shape[2]))
+    if len(shape) == 2:
+        return st[0] if shape[0] > 1 else max(st[0], shape[1])
+    b, n = shape[0], shape[1]
+    rs = st[1] if n > 1 else (st[0] if b > 1 else max(st[1], shape[2]))
     if b > 1 and n > 1 and st[0] != n * rs:
         raise ValueError(f"{name}: batch stride must be rows * row stride")
     return rs
 
 
-def _gs_io(dims):
-    import torch
-    if dims.io_dtype not in (MAMBA2_F32, MAMBA2_BF16):
-        raise ValueError("io_dtype: f32 or bf16")
-    return torch.float32 if dims.io_dtype == MAMBA2_F32 else torch.bfloat16
-
-
 def _gs_inputs(dims, shape, lam, x, r, g, z):
     """The shared inputs checked: their device, dtype and (pointer, row stride) arguments."""
     import torch
-    dt, dev = _gs_io(dims), x.device
+    if dims.io_dtype == MAMBA2_BF16:
+        dt = torch.bfloat16
+    elif dims.io_dtype == MAMBA2_F32:
+        dt = torch.float32
+    else:
+        raise ValueError("io_dtype: f32 or bf16")
+    dev = x.device
     if dev.type != "cuda":
         raise ValueError(f"x: a CUDA tensor expected, got {dev}")
     _need(lam, "lam", (dims.width,), torch.float32, dev)
-    rows = []
-    for name, t in (("x", x), ("r", r), ("g", g), ("z", z)):
-        if t is None and name == "z":
-            rows += [None, 0]
-            continue
-        _need(t, name, shape, dt, dev, contiguous=False)
-        rows += [t.data_ptr(), _row_stride(t, name)]
-    return dev, dt, rows
+    _need(x, "x", shape, dt, dev, False)
+    _need(r, "r", shape, dt, dev, False)
+    _need(g, "g", shape, dt, dev, False)
+    if z is None:
+        return dev, dt, (x.data_ptr(), _row_stride(x, "x"), r.data_ptr(), _row_stride(r, "r"),
+                         g.data_ptr(), _row_stride(g, "g"), None, 0)
+    _need(z, "z", shape, dt, dev, False)
+    return dev, dt, (x.data_ptr(), _row_stride(x, "x"), r.data_ptr(), _row_stride(r, "r"),
+                     g.data_ptr(), _row_stride(g, "g"), z.data_ptr(), _row_stride(z, "z"))
 
 
 class _On:
     """A call's surroundings: the tensors' device current and, where the caller names a stream,
     that stream too, so that what the call allocates belongs to the stream it is used on."""
 
+    __slots__ = ("other", "stream")
+
     def __init__(self, dev, stream):
         import torch
         self.other = None
-        if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = (torch.cuda.ExternalStream(int(stream), dev) if int(stream)
-                          else torch.cuda.default_stream(dev))
-            if stream.device != dev:
-                raise ValueError(f"stream: one of {dev} expected, got one of {stream.device}")
-            self.other = torch.cuda.stream(stream)
-            self.stream = stream.cuda_stream
-        else:
+        if stream is None:
             if torch.cuda.current_device() != dev.index:
                 self.other = torch.cuda.device(dev)
-            self.stream = torch.cuda.current_stream(dev).cuda_stream
+            # (the raw handle: a Stream object takes longer to make than a small kernel)
+            self.stream = torch._C._cuda_getCurrentRawStream(dev.index)
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = (torch.cuda.ExternalStream(int(stream), dev) if int(stream)
+                      else torch.cuda.default_stream(dev))
+        if stream.device != dev:
+            raise ValueError(f"stream: one of {dev} expected, got one of {stream.device}")
+        self.other = torch.cuda.stream(stream)
+        self.stream = stream.cuda_stream
 
     def __enter__(self):
         if self.other is not None:
@@ -680,7 +683,7 @@ def _state_cache_args(state, slots, codes, scales, block):
     b, (nslots, row) = state.shape[0], codes.shape
     if state.numel() != b * row:
         raise ValueError(f"state: {row} values a row expected, got {tuple(state.shape)}")
-    if b and not state[0].is_contiguous():
+    if not state.is_contiguous() and b and not state[0].is_contiguous():
         raise ValueError("state: each row's values must be contiguous")
     if block not in (32, 64, 128):
         raise ValueError("block: 32, 64 or 128")

@@ -26,11 +26,16 @@ namespace {
 static_assert(kGsChunk == 16, "tokens of a thread, between checkpoints");
 
 // ---------------------------------------------------------------- E at the chunks' ends
-// Nothing of a token is kept, so that a thread takes two chunks where shared memory lets
-// it: fewer tiles to look up.
-template <typename T> constexpr int kCarryTile = sizeof(T) == 2 ? 256 : 128;
-template <typename T, bool GATED> using CarryTiles = Shared<T, GATED ? 3 : 2, kCarryTile<T>>;
-template <bool GATED> constexpr int kCarryResident = GATED ? 2 : 3;
+// Nothing of a token is kept, so that a thread may take two chunks of 16: fewer, larger
+// tiles to look up (27 against 30 us at 4096 tokens of 5120 channels).  With z a stage of
+// such tiles would leave two blocks to an SM in place of four: there one chunk (78 against
+// 86 us at 8 rows of 2048 tokens and 4096 channels).
+template <typename T, bool GATED>
+constexpr int kCarryTile = sizeof(T) == 2 && !GATED ? 256 : 128;
+template <typename T, bool GATED>
+using CarryTiles = Shared<T, GATED ? 3 : 2, kCarryTile<T, GATED>>;
+template <typename T, bool GATED>
+constexpr int kCarryResident = GATED ? (sizeof(T) == 2 ? 4 : 2) : 3;
 
 __device__ __forceinline__ F2 silu2(F2 z) { return mul2(z, sigmoid2(z)); }
 
@@ -72,7 +77,7 @@ __device__ __forceinline__ float4 back_map(const unsigned char *in, const int *m
 }
 
 template <typename T, bool PACKED, bool GATED>
-__global__ void __launch_bounds__(kThreads, (kCarryResident<GATED>))
+__global__ void __launch_bounds__(kThreads, (kCarryResident<T, GATED>))
     gs_back_carry_kernel(const __grid_constant__ Maps maps, const Scan p, const float *dh,
                          float *carry) {
   using S = CarryTiles<T, GATED>;
@@ -432,10 +437,9 @@ struct BackPlan {
   size_t carry, ck, dl, sums, forward, total;
   int64_t partials;
 };
-BackPlan back_plan(int64_t rows, int64_t L, int D, int io, bool packed) {
+BackPlan back_plan(int64_t rows, int64_t L, int D, int io, bool packed, int carry_tile) {
   BackPlan b;
-  b.scan = plan_of(rows, L, D, io == MAMBA2_BF16 ? kCarryTile<__nv_bfloat16> : kCarryTile<float>,
-                   packed);
+  b.scan = plan_of(rows, L, D, carry_tile, packed);
   const size_t chunks = (size_t)(rows * ceil_div(L, kGsChunk)) * D * 4;
   const size_t width = (size_t)ceil_div(D, kApplyWidth) * kApplyWidth * 4;
   b.partials = rows * ceil_div(L, kApplyTile);
@@ -461,15 +465,16 @@ cudaError_t launch(const GatedScanBackwardArgs &b, const Scan &p, const float *c
       return cudaErrorInvalidValue;
   constexpr int kOf[3] = {1, 3, 4};  // r, dy, z
   for (int k = 0; k < (GATED ? 3 : 2); ++k)
-    if (!gs_tensor_map(&back.m[k], a.io, in[kOf[k]], rows, a.L, a.D, ld[kOf[k]], kWidth, kCarryTile<T>))
+    if (!gs_tensor_map(&back.m[k], a.io, in[kOf[k]], rows, a.L, a.D, ld[kOf[k]], kWidth,
+                       kCarryTile<T, GATED>))
       return cudaErrorInvalidValue;
   {
     constexpr size_t smem = sizeof(CarryTiles<T, GATED>);
-    static_assert((kCarryResident<GATED>)*(smem + 1024 + 256) <= 228 * 1024, "blocks to an SM");
+    static_assert((kCarryResident<T, GATED>)*(smem + 1024 + 256) <= 228 * 1024, "blocks to an SM");
     static ContextOnce once;
     const cudaError_t e = launch_dependent(
         gs_back_carry_kernel<T, PACKED, GATED>, once,
-        std::min(p.tiles, kCarryResident<GATED> * sm_count()), kThreads, smem, a.stream, back, p,
+        std::min(p.tiles, kCarryResident<T, GATED> * sm_count()), kThreads, smem, a.stream, back, p,
         b.dh, carry);
     if (e != cudaSuccess) return e;
   }
@@ -500,7 +505,9 @@ cudaError_t launch(const GatedScanBackwardArgs &b, const Scan &p, const float *c
 template <typename T> cudaError_t backward(const GatedScanBackwardArgs &b) {
   const GatedScanArgs &a = b.f;
   const bool packed = a.cu != nullptr;
-  const BackPlan w = back_plan(a.rows(), a.L, a.D, a.io, packed);
+  const BackPlan w =
+      back_plan(a.rows(), a.L, a.D, a.io, packed,
+                a.z != nullptr ? kCarryTile<T, true> : kCarryTile<T, false>);
   const float *ck = b.ck;
   if (ck == nullptr) {  // the forward again, for the states that enter the chunks
     GatedScanArgs f = a;
@@ -555,7 +562,7 @@ template <typename T> cudaError_t backward(const GatedScanBackwardArgs &b) {
 }  // namespace
 
 size_t gated_scan_backward_workspace(int64_t rows, int64_t L, int D, int io, bool packed) {
-  return back_plan(rows, L, D, io, packed).total;
+  return back_plan(rows, L, D, io, packed, 128).total;  // (the smaller of the tiles)
 }
 
 cudaError_t gated_scan_backward(const GatedScanBackwardArgs &b) {
