@@ -139,7 +139,7 @@ MAMBA2_API const char *mamba2_status_string(int status) {
   }
 }
 
-MAMBA2_API int mamba2_version(void) { return 100; }
+MAMBA2_API int mamba2_version(void) { return 200; }
 
 MAMBA2_API int mamba2_record_stage_events(void *const *events, int n_events) {
   if (n_events < 0 || n_events > kMaxStageEvents || (n_events > 0 && events == nullptr))

@@ -422,6 +422,88 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_row_does_not_depend_on_its_batch(dtype):
+    # the same numbers whatever else is in the call, forwards and back
+    D, L = 72, 1500
+    v = _inputs(5, L, D, 40, dtype, True)
+    h0, dh = _states(5, D, 41)
+    y, h, gr = _run(v, [L] * 5, D, dtype, False, h0, dh)
+    for i in (0, 3):
+        one = {k: (t if t is None or k == "lam" else t[i:i + 1].contiguous()) for k, t in v.items()}
+        y1, h1, gr1 = _run(one, [L], D, dtype, False, h0[i:i + 1], dh[i:i + 1])
+        assert torch.equal(y1[0], y[i]) and torch.equal(h1[0], h[i])
+        for k in ("x", "r", "g", "z", "h_state"):
+            assert torch.equal(gr1[k][0], gr[k][i]), k
+
+
+def test_nan_of_any_payload():
+    # blocks tell by a NaN pattern what has not been written yet: no input may look like it
+    D, L = 40, 1000
+    v = _inputs(1, L, D, 42, "f32", False)
+    bad = torch.tensor([-1], dtype=torch.int32, device="cuda").view(torch.float32)[0]
+    h0, dh = _states(1, D, 43)
+    for k in ("x", "r", "g", "dy", "h0", "dh", "lam"):
+        w, s, e = dict(v), h0.clone(), dh.clone()
+        if k == "h0":
+            s.fill_(bad)
+        elif k == "dh":
+            e.fill_(bad)
+        else:
+            w[k] = v[k].clone().fill_(bad)
+        y, h, gr = _run(w, [L], D, "f32", False, s, e)  # (no wait ran out)
+        assert torch.isnan(gr["h_state"]).all() if k in ("dh", "dy", "r", "lam") else True
+        if k in ("x", "r", "g", "h0", "lam"):
+            assert torch.isnan(y).all() and torch.isnan(h).all(), k
+
+
+def test_a_long_row():
+    D, L = 8, 70001
+    v = _inputs(1, L, D, 44, "f32", False)
+    h0, dh = _states(1, D, 45)
+    y, h, gr = _run(v, [L], D, "f32", False, h0, dh)
+    _compare(v, [L], "f32", False, h0, dh, y, h, gr)
+
+
+def test_more_sequences_than_65535():
+    D, n = 8, 70000
+    v = _inputs(None, n, D, 46, "f32", False)
+    h0, dh = _states(n, D, 47)
+    y, h, gr = _run(v, [1] * n, D, "f32", True, h0, dh)
+    # single tokens: the recurrence once, for all of them side by side
+    lam = _np(v["lam"])
+    R, G, la, a, m = GS._gates(lam, _np(v["r"]), _np(v["g"]), C)
+    want = a * _np(h0) + m * G * _np(v["x"])
+    off = 2 * GS.KAPPA * GS.U * (a * np.abs(_np(h0)) + m * G * np.abs(_np(v["x"])))
+    _check(y, want, off, "y")
+    _check(h, want, off, "h")
+    d = _np(v["dy"]) + _np(dh)
+    _check(gr["h_state"], a * d, 3 * GS.KAPPA * GS.U * a * (np.abs(_np(v["dy"])) + np.abs(_np(dh))),
+           "dh0")
+
+
+def test_waits_that_run_out_are_reported():
+    D, L = 200, 900
+    v = _inputs(2, L, D, 48, "bf16", True)
+    h0, dh = _states(2, D, 49)
+    assert m2.device_errors() == 0
+    dims = m2.make_gated_scan_dims(2, L, D)
+    m2.debug_stall_waits(True)
+    try:
+        y = torch.full((2, L, D), 3.0, device="cuda", dtype=torch.bfloat16)
+        m2.gated_scan_prefill(dims, v["lam"], v["x"], v["r"], v["g"], z=v["z"], y=y)
+        assert m2.device_errors() & 1
+        assert (y == 3).all()
+        ck = m2.gated_scan_checkpoints(dims).zero_()
+        m2.gated_scan_backward(dims, v["lam"], v["x"], v["r"], v["g"], v["dy"], z=v["z"],
+                               checkpoints=ck)
+        assert m2.device_errors() & 1
+    finally:
+        m2.debug_stall_waits(False)
+    assert m2.device_errors() == 0
+    _compare(v, [L, L], "bf16", False, h0, dh, *_run(v, [L, L], D, "bf16", False, h0, dh))
+
+
 def test_binding_refuses_what_does_not_fit():
     D, L = 32, 10
     v = _inputs(2, L, D, 32, "bf16", False)
