@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
     float4 map;
     const bool close = __all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f);
     if (close && n == S::kTile) map = make_maps<S, true, true>(in, k, n - first, a, b);
+    else if (close) map = make_maps<S, false, true>(in, k, n - first, a, b);
     else map = make_maps<S, false, false>(in, k, n - first, a, b);
     if (PACKED && !whole) map = reset_maps<S>(marks, begins, p, d, a, b);
     sm.seg[half][seg][lane] = map;
@@ -189,11 +190,77 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
   }
 }
 
-// ---------------------------------------------------------------- decode
 template <typename T> struct In {
   const T *x, *r, *g, *z;
   int64_t ld_x, ld_r, ld_g, ld_z;
 };
+
+// ---------------------------------------------------------------- short rows
+// A thread runs the tokens of a row for two channels, four tokens' loads at a time: tiles
+// would be mostly empty, and nothing has to be prepared.
+constexpr int kShortBatch = 4;
+template <typename T, bool GATED>
+__global__ void __launch_bounds__(128, 5)
+    gs_short_kernel(In<T> in, const float *__restrict__ lam, float c, int64_t pairs, int L, int D,
+                    const float *h_in, float *h_out, float *__restrict__ ck, T *__restrict__ y) {
+  using V = typename Pair<T>::V;
+  const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (at >= pairs) return;
+  const int64_t row = at / (D / 2), nch = (L + kGsChunk - 1) / kGsChunk;
+  const int d = 2 * (int)(at % (D / 2));
+  const T *x = in.x + row * L * in.ld_x + d, *r = in.r + row * L * in.ld_r + d,
+          *g = in.g + row * L * in.ld_g + d, *z = in.z + (GATED ? row * L * in.ld_z + d : 0);
+  T *out = y + row * L * D + d;
+  F2 h = f2(0.0f);
+  if (h_in != nullptr) {
+    const float2 v = *reinterpret_cast<const float2 *>(h_in + row * D + d);
+    h = f2(v.x, v.y);
+  }
+  const F2 ncs = f2(-c * softplus_f(lam[d]) * kLog2e, -c * softplus_f(lam[d + 1]) * kLog2e);
+  auto run = [&](auto near) {
+#pragma unroll 1
+    for (int t0 = 0; t0 < L; t0 += kShortBatch) {
+      const int n = min(kShortBatch, L - t0);
+      V bx[kShortBatch], br[kShortBatch], bg[kShortBatch], bz[kShortBatch];
+#pragma unroll
+      for (int i = 0; i < kShortBatch; ++i)
+        if (i < n) {
+          bx[i] = *reinterpret_cast<const V *>(x + i * in.ld_x);
+          br[i] = *reinterpret_cast<const V *>(r + i * in.ld_r);
+          bg[i] = *reinterpret_cast<const V *>(g + i * in.ld_g);
+          if (GATED) bz[i] = *reinterpret_cast<const V *>(z + i * in.ld_z);
+        }
+      if (ck != nullptr && t0 % kGsChunk == 0)
+        *reinterpret_cast<float2 *>(ck + (row * nch + t0 / kGsChunk) * D + d) = unpack(h);
+#pragma unroll
+      for (int i = 0; i < kShortBatch; ++i)
+        if (i < n) {
+          const Coeffs k = coefficients<decltype(near)::value>(gs_pair<T>(&bx[i]), gs_clamped<T>(&br[i]),
+                                               gs_clamped<T>(&bg[i]), ncs);
+          h = fma2(k.a, h, k.b);
+          if (y != nullptr) {
+            F2 o = h;
+            if (GATED) {
+              const F2 zz = gs_pair<T>(&bz[i]);
+              o = mul2(h, mul2(zz, sigmoid2(zz)));
+            }
+            store_pair(out + (int64_t)i * D, unpack(o));
+          }
+        }
+      x += kShortBatch * in.ld_x;
+      r += kShortBatch * in.ld_r;
+      g += kShortBatch * in.ld_g;
+      if (GATED) z += kShortBatch * in.ld_z;
+      out += (int64_t)kShortBatch * D;
+    }
+  };
+  const float2 k2 = unpack(ncs);
+  if (__all_sync(__activemask(), fminf(k2.x, k2.y) >= -0.5f)) run(std::true_type());
+  else run(std::false_type());
+  if (h_out != nullptr) *reinterpret_cast<float2 *>(h_out + row * D + d) = unpack(h);
+}
+
+// ---------------------------------------------------------------- decode
 
 // 16 bytes of a row: V = 4 or 8 channels.
 template <typename T> struct Lane {
@@ -280,8 +347,24 @@ cudaError_t launch(const GatedScanArgs &a, const Maps &m, const Scan &p) {
                           a.ck);
 }
 
+// Rows for gs_short_kernel.  It wins where tiles of 128 tokens are mostly empty: up to 16
+// tokens always (one row of 16 tokens and 5120 channels 4.9 us against 7.0, 64 rows 15
+// against 67), up to 64 where there are threads for the whole GPU (64 rows of 64 tokens 51
+// against 67 us); one row of 64 tokens is slower by it (13.7 against 6.9 us), and 64 rows
+// of 128 tokens too (96 against 64 us).
+constexpr int64_t kShort = 16, kShortOfMany = 64, kMany = 65536;
+
 template <typename T> cudaError_t prefill(const GatedScanArgs &a) {
   const int64_t rows = a.rows();
+  const int64_t pairs = rows * (a.D / 2);
+  if (a.cu == nullptr && (a.L <= kShort || (a.L <= kShortOfMany && pairs >= kMany))) {
+    const auto kernel = a.z != nullptr && a.y != nullptr ? gs_short_kernel<T, true>
+                                                         : gs_short_kernel<T, false>;
+    kernel<<<(unsigned)ceil_div(pairs, 128), 128, 0, a.stream>>>(
+        inputs<T>(a), a.lam, a.c, pairs, (int)a.L, a.D, a.states_in ? a.h : nullptr,
+        a.no_state_out ? nullptr : a.h, a.ck, static_cast<T *>(a.y));
+    return cudaGetLastError();
+  }
   const bool packed = a.cu != nullptr, gated = a.z != nullptr && a.y != nullptr;
   const Plan w = plan_of(rows, a.L, a.D, Tiles<T, false>::kTile, packed);
   Maps m = {};
