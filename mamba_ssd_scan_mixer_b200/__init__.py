@@ -494,25 +494,31 @@ def _row_stride(t, name):
 def _gs_inputs(dims, shape, lam, x, r, g, z):
     """The shared inputs checked: their device, dtype and (pointer, row stride) arguments."""
     import torch
-    if dims.io_dtype == MAMBA2_BF16:
-        dt = torch.bfloat16
-    elif dims.io_dtype == MAMBA2_F32:
-        dt = torch.float32
-    else:
-        raise ValueError("io_dtype: f32 or bf16")
+    f32, width = torch.float32, dims.width
+    dt = torch.bfloat16 if dims.io_dtype == MAMBA2_BF16 else f32
     dev = x.device
-    if dev.type != "cuda":
-        raise ValueError(f"x: a CUDA tensor expected, got {dev}")
-    _need(lam, "lam", (dims.width,), torch.float32, dev)
-    _need(x, "x", shape, dt, dev, False)
-    _need(r, "r", shape, dt, dev, False)
-    _need(g, "g", shape, dt, dev, False)
-    if z is None:
-        return dev, dt, (x.data_ptr(), _row_stride(x, "x"), r.data_ptr(), _row_stride(r, "r"),
-                         g.data_ptr(), _row_stride(g, "g"), None, 0)
-    _need(z, "z", shape, dt, dev, False)
-    return dev, dt, (x.data_ptr(), _row_stride(x, "x"), r.data_ptr(), _row_stride(r, "r"),
-                     g.data_ptr(), _row_stride(g, "g"), z.data_ptr(), _row_stride(z, "z"))
+    # (one expression for what is nearly always so; what is not is then told apart)
+    if not (x.is_cuda and x.dtype is dt and r.dtype is dt and g.dtype is dt and lam.dtype is f32
+            and x.shape == shape and r.shape == shape and g.shape == shape
+            and r.device == dev and g.device == dev and lam.device == dev
+            and lam.shape == (width,) and lam.is_contiguous()
+            and dims.io_dtype in (MAMBA2_F32, MAMBA2_BF16)):
+        if dims.io_dtype not in (MAMBA2_F32, MAMBA2_BF16):
+            raise ValueError("io_dtype: f32 or bf16")
+        if not x.is_cuda:
+            raise ValueError(f"x: a CUDA tensor expected, got {dev}")
+        _need(lam, "lam", (width,), f32, dev)
+        for name, t in (("x", x), ("r", r), ("g", g)):
+            _need(t, name, shape, dt, dev, False)
+    if z is not None:
+        _need(z, "z", shape, dt, dev, False)
+    if len(shape) == 2 and shape[0] > 1:  # rows of tokens one after the other
+        sx, sr, sg = x.stride(), r.stride(), g.stride()
+        if sx[1] == 1 and sr[1] == 1 and sg[1] == 1 and z is None:
+            return dev, dt, (x.data_ptr(), sx[0], r.data_ptr(), sr[0], g.data_ptr(), sg[0], None, 0)
+    rows = (x.data_ptr(), _row_stride(x, "x"), r.data_ptr(), _row_stride(r, "r"),
+            g.data_ptr(), _row_stride(g, "g"))
+    return dev, dt, rows + ((None, 0) if z is None else (z.data_ptr(), _row_stride(z, "z")))
 
 
 class _On:
@@ -593,7 +599,7 @@ def gated_scan_prefill(dims, lam, x, r, g, z=None, h_state=None, states_in=False
         _need(y, "y", shape, dt, dev)
     with _On(dev, stream) as s:
         if y is None:
-            y = torch.empty(shape, dtype=dt, device=dev)
+            y = torch.empty(*shape, dtype=dt, device=dev)
         ws, ws_at, ws_bytes = _scratch(workspace, mamba2_gated_scan_workspace_size(dims, packed),
                                        dev)
         st = lib().mamba2_gated_scan_prefill(
@@ -613,11 +619,18 @@ def gated_scan_step(dims, lam, x, r, g, h_state, z=None, y=None, stream=None):
     _need(h_state, "h_state", shape, torch.float32, dev)
     if y is not None:
         _need(y, "y", shape, dt, dev)
-    with _On(dev, stream) as s:
+    if stream is None and torch.cuda.current_device() == dev.index:
         if y is None:
-            y = torch.empty(shape, dtype=dt, device=dev)
+            y = torch.empty(*shape, dtype=dt, device=dev)
         st = lib().mamba2_gated_scan_step(ctypes.byref(dims), lam.data_ptr(), *rows, y.data_ptr(),
-                                          h_state.data_ptr(), s)
+                                          h_state.data_ptr(),
+                                          torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with _On(dev, stream) as s:
+            if y is None:
+                y = torch.empty(*shape, dtype=dt, device=dev)
+            st = lib().mamba2_gated_scan_step(ctypes.byref(dims), lam.data_ptr(), *rows,
+                                              y.data_ptr(), h_state.data_ptr(), s)
     if st != 0:
         raise Mamba2Error(st, "mamba2_gated_scan_step")
     return y
@@ -638,7 +651,7 @@ def gated_scan_backward(dims, lam, x, r, g, dy, z=None, h_state_in=None, d_h_sta
     _gs_optional(dims, packed, cu_seqlens,
                  (("h_state_in", h_state_in), ("d_h_state_out", d_h_state_out)), checkpoints, dev)
     with _On(dev, stream) as s:
-        grads = {k: torch.empty(shape, dtype=dt, device=dev)
+        grads = {k: torch.empty(*shape, dtype=dt, device=dev)
                  for k in (("x", "r", "g") if z is None else ("x", "r", "g", "z"))}
         grads["lam"] = torch.empty(dims.width, dtype=torch.float32, device=dev)
         if h_state_in is not None:
@@ -673,12 +686,12 @@ def state_cache(nslots, row, block=64, codes="int8", device="cuda"):
 
 def _state_cache_args(state, slots, codes, scales, block):
     import torch
-    dev = state.device
-    if dev.type != "cuda":
+    dev, sdt, cdt = state.device, state.dtype, codes.dtype
+    if not state.is_cuda:
         raise ValueError(f"state: a CUDA tensor expected, got {dev}")
-    if state.dim() < 2 or state.dtype not in (torch.float32, torch.bfloat16):
+    if state.dim() < 2 or (sdt is not torch.float32 and sdt is not torch.bfloat16):
         raise ValueError("state: [b, ...] of fp32 or bf16 expected")
-    if codes.dim() != 2 or codes.dtype not in (torch.int8, torch.float8_e4m3fn):
+    if codes.dim() != 2 or (cdt is not torch.int8 and cdt is not torch.float8_e4m3fn):
         raise ValueError("codes: [slots, row] of int8 or float8_e4m3fn expected")
     b, (nslots, row) = state.shape[0], codes.shape
     if state.numel() != b * row:
@@ -687,11 +700,15 @@ def _state_cache_args(state, slots, codes, scales, block):
         raise ValueError("state: each row's values must be contiguous")
     if block not in (32, 64, 128):
         raise ValueError("block: 32, 64 or 128")
-    _need(slots, "slots", (b,), torch.int32, dev)
-    _need(codes, "codes", codes.shape, codes.dtype, dev)
-    _need(scales, "scales", (nslots, -(-row // block)), torch.uint8, dev)
-    dims = Mamba2StateCacheDims(b, row, nslots, int(block), int(codes.dtype != torch.int8),
-                                MAMBA2_F32 if state.dtype == torch.float32 else MAMBA2_BF16)
+    if not (slots.shape == (b,) and slots.dtype is torch.int32 and slots.device == dev
+            and slots.is_contiguous() and codes.device == dev and codes.is_contiguous()
+            and scales.dtype is torch.uint8 and scales.device == dev and scales.is_contiguous()
+            and scales.shape == (nslots, -(-row // block))):
+        _need(slots, "slots", (b,), torch.int32, dev)
+        _need(codes, "codes", codes.shape, cdt, dev)
+        _need(scales, "scales", (nslots, -(-row // block)), torch.uint8, dev)
+    dims = Mamba2StateCacheDims(b, row, nslots, block, 0 if cdt is torch.int8 else 1,
+                                MAMBA2_F32 if sdt is torch.float32 else MAMBA2_BF16)
     return dev, dims, state.stride(0) if b > 1 else row
 
 

@@ -354,10 +354,14 @@ inline cudaError_t prepare(const GatedScanArgs &a, const Plan &w, char *ws, cons
 }
 
 inline int sm_count() {
+  static std::atomic<int> known[64] = {};
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 148;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
   return n;
 }
 
