@@ -63,21 +63,6 @@ inline int64_t gs_tiles(int64_t rows, int64_t L, int64_t D) {
 // ---------------------------------------------------------------- arithmetic
 __device__ __forceinline__ float gs_sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
 
-struct Gate {
-  float R, G, la, a, m;
-};
-// `ncs` = -c softplus(lam).  1 - a^2 comes from expm1, so that it keeps its
-// relative accuracy where a is next to one.
-__device__ __forceinline__ Gate gs_gate(float r, float g, float ncs) {
-  Gate q;
-  q.R = gs_sigmoid(r);
-  q.G = gs_sigmoid(g);
-  q.la = ncs * q.R;
-  q.a = expf(q.la);
-  q.m = sqrtf(-expm1f(2.0f * q.la));
-  return q;
-}
-
 // Pairs of fp32 values in one 64-bit register: two multiply-adds an instruction.
 struct F2 {
   unsigned long long v;
@@ -358,38 +343,8 @@ template <> struct Pair<__nv_bfloat16> {
     return __floats2bfloat162_rn(a, b);
   }
 };
-template <typename T> __device__ __forceinline__ float2 ld2(const T *p) {
-  return Pair<T>::get(*reinterpret_cast<const typename Pair<T>::V *>(p));
-}
 template <typename T> __device__ __forceinline__ void st2(T *p, float2 v) {
   *reinterpret_cast<typename Pair<T>::V *>(p) = Pair<T>::put(v.x, v.y);
-}
-template <typename T> __device__ __forceinline__ void st2(T *p, float a, float b) {
-  *reinterpret_cast<typename Pair<T>::V *>(p) = Pair<T>::put(a, b);
-}
-
-// The sequences that begin or end inside tokens [t0, t0 + n) of packed rows:
-// first[i] / last[i] = the sequence whose first / last token is t0 + i, else
-// -1.  Called by the whole block; `n` <= kGsChunk.
-__device__ __forceinline__ void gs_marks(const int32_t *cu, int64_t batch, int64_t t0, int n,
-                                         int *first, int *last) {
-  for (int i = threadIdx.x; i < n; i += blockDim.x) first[i] = last[i] = -1;
-  // the first sequence that ends after t0
-  int64_t lo = 0, hi = batch;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (cu[mid + 1] > t0) hi = mid;
-    else lo = mid + 1;
-  }
-  __syncthreads();
-  for (int64_t s = lo + threadIdx.x; s < batch; s += blockDim.x) {
-    const int64_t b = cu[s], e = cu[s + 1];
-    if (b >= t0 + n) break;
-    if (e <= b) continue;
-    if (b >= t0) first[b - t0] = (int)s;
-    if (e - 1 >= t0 && e - 1 < t0 + n) last[e - 1 - t0] = (int)s;
-  }
-  __syncthreads();
 }
 
 }  // namespace m2

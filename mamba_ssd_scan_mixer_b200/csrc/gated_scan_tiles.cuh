@@ -76,7 +76,7 @@ template <typename T_, int TENSORS, int TOKENS> struct Shared {
 __global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, uint4 *records,
                                int64_t nrecords, unsigned int *ticket, const int32_t *cu, int64_t batch,
                                int64_t L, int *marks, unsigned int *bad,
-                               const float *first, const float *empty_in, float *empty_out) {
+                               const float *empty_in, float *empty_out) {
   launch_dependents();
   const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t all = (int64_t)gridDim.x * blockDim.x;
@@ -96,12 +96,6 @@ __global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, uin
     if (wrong) atomicOr(&g_gs_errors, kErrSeqlens);
   }
   if (wrong) return;
-  // the sequences' states into L2: each is wanted at once when its first token comes up,
-  // and tiles of the whole row wait for it (2 us a sequence without this)
-  constexpr int64_t kMostPrefetched = 32 << 20;
-  if (first != nullptr && batch * D * 4 <= kMostPrefetched)
-    for (int64_t i = at * 32; i < batch * D; i += all * 32)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(first + i));
   for (int64_t t = at; t < L; t += all) {
     int64_t lo = 0, hi = batch - 1;  // the sequence of token t: the first that ends after it
     while (lo < hi) {
@@ -123,7 +117,7 @@ __global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, uin
 __device__ __forceinline__ void segments_done() {  // the computing warps
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
 }
-__device__ __forceinline__ void entered_wait(int half) {  // the computing warps, for the ninth
+__device__ __forceinline__ void entered_wait(int half) {  // the computing warps, for the fifth
   asm volatile("bar.sync %0, %1;" ::"r"(2 + half), "n"(kThreads) : "memory");
 }
 __device__ __forceinline__ void entered_signal(int half) {
@@ -349,7 +343,7 @@ inline cudaError_t prepare(const GatedScanArgs &a, const Plan &w, char *ws, cons
   gs_prep_kernel<<<(unsigned)std::min<int64_t>(ceil_div(work, 256), 148 * 4), 256, 0, a.stream>>>(
       a.lam, a.c, a.D, const_cast<float *>(p->ncs), reinterpret_cast<uint4 *>(ws + w.maps),
       nrecords, p->ticket, a.cu, a.batch, a.L, const_cast<int *>(p->marks),
-      const_cast<unsigned int *>(p->bad), first, empty_in, empty_out);
+      const_cast<unsigned int *>(p->bad), empty_in, empty_out);
   return cudaGetLastError();
 }
 
