@@ -14,10 +14,15 @@
 //   2. gs_back_apply_kernel then has, for each 16 tokens, the state that enters them (the
 //      prefill's checkpoints) and the E that does: its warps depend on nobody.  Each runs
 //      its 16 tokens forwards, keeping h, R and G in registers, and backwards.
-// The first pass costs 4 bytes an element beside the second's 14 (bf16), but the second
-// begins where the first ended, with the tokens whose r and dy are still in L2.  One pass
-// over everything would have to keep a tile's coefficients while the E entering it is
-// looked up, which halves the tiles under way.
+// The first pass costs 4 bytes an element beside the second's 14 (bf16).  (The second
+// begins where the first ended, and finds 29 of 84 MB of r and dy in L2 at 4096 tokens of
+// 5120 channels.)  One pass over everything would have to keep a tile's coefficients while
+// the E entering it is looked up, which halves the tiles under way.
+//
+// 4096 tokens of 5120 channels, bf16: the first 27 us (13 at the copy rate), the second
+// 65 us (46).  The first waits for the maps of the tiles before, as the prefill does.  The
+// second issues 114 instructions a pair of channels and token, 12 of them ex2, rcp or sqrt,
+// at 55% of the issue rate with the 12 warps that its registers leave.
 #include "gated_scan_tiles.cuh"
 
 namespace m2 {

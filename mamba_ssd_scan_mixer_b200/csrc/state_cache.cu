@@ -6,6 +6,11 @@
 // A power of two makes v 2^-e exact, so the only rounding is the code's own (to
 // nearest, ties to even), and a state that was read back and is written again
 // gives the same values.
+//
+// Bytes bound both ways.  256 SSM states of 80 x 64 x 64 in fp32 (336 MB) into int8: 76 us,
+// 5.5 TB/s; back: 69 us, 6.1 TB/s.  bf16: 48 and 44 us.  What a store lacks to the copy rate
+// is the maximum that each block's values wait for, and the search for a later row of the
+// same slot.
 #include <cuda_fp8.h>
 
 #include "state_cache.cuh"
@@ -214,7 +219,8 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Rows anywhere: a lane takes single values, 32 apart, so that a warp's loads and
+// Rows anywhere (a row of 327679 values: stores 109 us fp32, 112 us bf16, loads 112 us, with
+// the 16-byte lanes of the same sizes at 76, 48 and 69): a lane takes single values, 32 apart, so that a warp's loads and
 // stores are of neighbouring ones; a warp has kPer * 32 values (whole blocks) under
 // way.
 constexpr int kPer = 8;
