@@ -22,8 +22,6 @@
 // row the tiles under way reach over four steps of the row, and each waits about a
 // microsecond a round for the map of the one before (43 us, 60%).  Next to that come the
 // instructions: 47 a pair of channels and token, eight of them ex2, rcp or sqrt.
-#include <type_traits>
-
 #include "gated_scan_tiles.cuh"
 
 namespace m2 {

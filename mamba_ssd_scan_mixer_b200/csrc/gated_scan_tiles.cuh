@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gated_scan.cuh"
 
@@ -30,7 +31,7 @@ constexpr int kThreads = 32 * (kWarps + 1);
 // 32768 tokens of 64 channels; equal at 768).
 constexpr int kNear = 8, kFar = 32;
 constexpr int kFarBelow = 24;  // tiles of a step
-constexpr int kBatch = 8;      // maps read at once
+constexpr int kBatch = 4;      // maps read at once
 
 // Bits of a token's mark in packed rows: (sequence << 2) | last << 1 | first.
 constexpr int kFirst = 1, kLast = 2;
@@ -38,6 +39,17 @@ constexpr int kFirst = 1, kLast = 2;
 struct Maps {
   CUtensorMap m[5];
 };
+
+// Division of numbers below 2^30 by one known on the host.
+struct Divide {
+  unsigned long long m;
+  __device__ __forceinline__ int of(int t) const {
+    return m == 0 ? t : (int)__umul64hi((unsigned long long)t, m);
+  }
+};
+inline Divide divide_by(int d) {  // floor(2^64 / d) + 1: exact while t d < 2^64
+  return Divide{d == 1 ? 0 : ~0ull / (unsigned)d + 1};
+}
 
 struct Scan {
   const float *ncs;  // -c softplus(lam) log2(e) of each channel, padded with zeros
@@ -49,6 +61,7 @@ struct Scan {
   float4 *maps;             // [tiles][kLanes]: the tiles' maps
   float2 *states;           // [tiles][kLanes]: the states they leave
   unsigned int *ticket;
+  Divide by_nblk, by_rows;
 };
 
 struct Tile {
@@ -202,10 +215,11 @@ __device__ __forceinline__ void look_up(S &sm, const Maps &in, const Scan &p) {
   // one lane: tile t's copies, into stage s
   auto fetch = [&](int s, int t) {
     Tile q;
+    const int of_rows = p.by_nblk.of(t);
     q.left = p.tiles - t;
-    q.cb = t % p.nblk;
-    q.row = t / p.nblk % p.rows;
-    q.step = t / per_step;
+    q.cb = t - of_rows * p.nblk;
+    q.step = p.by_rows.of(of_rows);
+    q.row = of_rows - q.step * p.rows;
     sm.tile[s] = q;
     if (q.left <= 0) {
       mbar_arrive(&sm.full[s]);
@@ -241,63 +255,74 @@ __device__ __forceinline__ void look_up(S &sm, const Maps &in, const Scan &p) {
     const int d = q.cb * kWidth + 2 * l;
     const int tile = q.step * per_step + q.row * p.nblk + q.cb;
     const int between = min(q.step, p.back - 1);
-    bool fetched = false, entered = false, based = q.step < p.back;
+    bool fetched = false, entered = false, based = q.step < p.back, alive = true;
     int folded = 0;  // maps, of those between
-    const float2 *base = p.states + ((int64_t)tile - (int64_t)p.back * per_step) * kLanes + l;
-    const float4 *maps = p.maps + ((int64_t)tile - (int64_t)between * per_step) * kLanes + l;
+    const int64_t stride = (int64_t)per_step * kLanes;
+    const float2 *base = p.states + (int64_t)tile * kLanes + l - p.back * stride;
+    const float4 *maps = p.maps + (int64_t)tile * kLanes + l - between * stride;
     float2 h = make_float2(0.0f, 0.0f);
     if (!PACKED && q.step == 0 && p.first != nullptr && d < p.D)
       h = *reinterpret_cast<const float2 *>(p.first + (int64_t)q.row * p.D + d);
+    // asks for the next maps (and the base), and folds those that are there without a gap
+    auto ask = [&]() {
+      float2 b = make_float2(0.0f, 0.0f);
+      float4 m[kBatch];
+      if (!based) b = record_get(base);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (folded + k < between) m[k] = record_get(maps + k * stride);
+      unsigned int there = based || is_set(b) ? 1u << 31 : 0u;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (folded + k < between && is_set(m[k])) there |= 1u << k;
+      there = __reduce_and_sync(0xffffffffu, there);
+      if (!(there >> 31)) return;
+      if (!based) h = b;
+      based = true;
+      const int run = __ffs(~there) - 1;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (k < run) h = gs_through(m[k], h);
+      folded += run;
+      maps += run * stride;
+      entered = folded == between;
+      if (entered) {
+        sm.enter[half][l] = h;
+        entered_signal(half);
+      }
+    };
+    auto refill = [&]() {
+      if (lane == 0) fetch(s, next);  // every warp is done with the stage
+      __syncwarp();
+      fetched = true;
+    };
+    // Few instructions here count, and short code: this warp shares its scheduler with a
+    // computing one, for which the others wait, and the instruction cache with all.
     unsigned long long since = 0;
-    for (;;) {
-      if (!entered) {
-        float2 b = make_float2(0.0f, 0.0f);
-        float4 m[kBatch];
-        if (!based) b = record_get(base);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          if (folded + k < between) m[k] = record_get(maps + (int64_t)(folded + k) * per_step * kLanes);
-        unsigned int there = based || is_set(b) ? 1u << 31 : 0u;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          if (folded + k < between && is_set(m[k])) there |= 1u << k;
-        there = __reduce_and_sync(0xffffffffu, there);
-        if (there >> 31) {
-          if (!based) h = b;
-          based = true;
-          const int run = __ffs(~there) - 1;  // maps there without a gap
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k)
-            if (k < run) h = gs_through(m[k], h);
-          folded += run;
-          entered = folded == between;
-        }
-        if (entered) {
-          sm.enter[half][l] = h;
-          entered_signal(half);
-        }
+    for (int asked = 0; !entered && alive; ++asked) {
+      if (!fetched && __all_sync(0xffffffffu, mbar_test(&sm.segs[half], phase))) refill();
+      ask();
+      if (asked % 64 == 63) {
+        const unsigned long long now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
+        if (since == 0) since = now;
+        alive = now - since <= kWaitLimitNs;
       }
-      if (!fetched && __all_sync(0xffffffffu, entered ? mbar_try_wait(&sm.segs[half], phase)
-                                                      : mbar_test(&sm.segs[half], phase))) {
-        if (lane == 0) fetch(s, next);  // every warp is done with the stage
-        __syncwarp();
-        fetched = true;
+    }
+    if (alive && !fetched) {
+      alive = __all_sync(0xffffffffu, mbar_wait_bounded(&sm.segs[half], phase, &g_gs_errors));
+      if (alive) refill();
+    }
+    if (!alive) {
+      // what this block has under way lands before the warp leaves, and nobody waits for it
+      sm.dead = 1;
+      __syncwarp();
+      entered_signal(entered ? half ^ 1 : half);
+      if (lane == 0) {
+        atomicOr(&g_gs_errors, kErrWaitTimeout);
+        for (int i = it + fetched; i < it + fetched + S::kStages; ++i)
+          mbar_wait_bounded(&sm.full[i % S::kStages], (i / S::kStages) & 1, &g_gs_errors);
       }
-      if (fetched && entered) break;
-      const unsigned long long now = globaltimer_ns();
-      if (since == 0) since = now;
-      if (__any_sync(0xffffffffu, now - since > kWaitLimitNs)) {
-        // what this block has under way lands before the warp leaves, and nobody waits for it
-        sm.dead = 1;
-        __syncwarp();
-        entered_signal(entered ? half ^ 1 : half);
-        if (lane == 0) {
-          atomicOr(&g_gs_errors, kErrWaitTimeout);
-          for (int i = it + fetched; i < it + fetched + S::kStages; ++i)
-            mbar_wait_bounded(&sm.full[i % S::kStages], (i / S::kStages) & 1, &g_gs_errors);
-        }
-        return;
-      }
+      return;
     }
   }
 }
@@ -339,6 +364,8 @@ inline cudaError_t prepare(const GatedScanArgs &a, const Plan &w, char *ws, cons
   p->ticket = reinterpret_cast<unsigned int *>(ws);
   p->bad = p->ticket + 1;
   p->first = first;
+  p->by_nblk = divide_by(w.nblk);
+  p->by_rows = divide_by(p->rows);
   p->maps = reinterpret_cast<float4 *>(ws + w.maps);
   p->states = reinterpret_cast<float2 *>(ws + w.states);
   const int64_t nrecords = (int64_t)(w.marks - w.maps) / 16;  // maps and states, side by side
