@@ -205,6 +205,8 @@ def _train(s):
         grads = m2.gated_scan_backward(dims, s["lam"], s["x"], s["r"], s["g"], s["dy"], z=s["z"],
                                        h_state_in=s["h0"], d_h_state_out=s["dh"],
                                        cu_seqlens=s["cu"], checkpoints=ck)
+        if s["cu"] is not None and s["z"] is not None:
+            grads["z"] = grads["z"][None]  # laid out as the plain form gives it: one row
         return {"y": y, **{"d_" + k: v for k, v in grads.items()}}
     y, _, h, h_prev, first, last = _forward(s, s["h0"])
     a, m, la, R, G = _gates(s)
