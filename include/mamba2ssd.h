@@ -415,7 +415,11 @@ MAMBA2_API size_t mamba2_gated_scan_checkpoint_count(const mamba2_gated_scan_dim
  *          before, whatever its sequence; token 0's is zero.)
  *  workspace  >= mamba2_gated_scan_workspace_size bytes, 256-byte aligned;
  *          contents on entry are ignored.  stream: cudaStream_t as void*.
- * Results do not depend on timing: every sum has a fixed order. */
+ * Results do not depend on timing: every sum has a fixed order.  (Rows of at most
+ * 64 tokens may be summed in another order in a large batch than in a small one.)
+ * Range: a gate sigmoid below 2^-62 counts as 2^-62, and where 1 - a^2 is below
+ * 2^-56 nothing is added: r = -infinity keeps a state as it is (for c softplus(lam)
+ * < 32).  NaN and infinities stay within their sequence and channel. */
 MAMBA2_API int mamba2_gated_scan_prefill(
     const mamba2_gated_scan_dims *dims, const float *lam, const void *x, int64_t x_row_stride,
     const void *r, int64_t r_row_stride, const void *g, int64_t g_row_stride, const void *z,
@@ -423,7 +427,8 @@ MAMBA2_API int mamba2_gated_scan_prefill(
     float *checkpoints, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Decode: one token of each sequence.  x, r, g, z: [b, D] as above; y [b, D]
- * contiguous; h_state [b, D] fp32, updated in place.  Uses no workspace. */
+ * contiguous; h_state [b, D] fp32, updated in place.  At most 524280 sequences.
+ * Uses no workspace. */
 MAMBA2_API int mamba2_gated_scan_step(const mamba2_gated_scan_dims *dims, const float *lam,
                                       const void *x, int64_t x_row_stride, const void *r,
                                       int64_t r_row_stride, const void *g, int64_t g_row_stride,
@@ -443,7 +448,8 @@ MAMBA2_API int mamba2_gated_scan_step(const mamba2_gated_scan_dims *dims, const 
  *  d_x, d_r, d_g, d_z  [b, L, D] io_dtype, contiguous, 16-byte aligned (d_z only
  *          with z, else NULL); d_lam [D] fp32; d_h_state_in [b, D] fp32 or NULL.
  * All states and their gradients are 16-byte aligned.  With invalid cu_seqlens
- * nothing is written (bit 2 as above).  Results do not depend on timing. */
+ * nothing is written (bit 2 as above).  Results do not depend on timing.  A gate
+ * shut by r = -infinity gets a zero gradient. */
 MAMBA2_API int mamba2_gated_scan_backward(
     const mamba2_gated_scan_dims *dims, const float *lam, const void *x, int64_t x_row_stride,
     const void *r, int64_t r_row_stride, const void *g, int64_t g_row_stride, const void *z,

@@ -421,8 +421,8 @@ __global__ void __launch_bounds__(32 * kSumGroups)
   if (bad != nullptr && *bad) return;
   __shared__ float part[kSumGroups][33];
   const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
-  const int d = blockIdx.x * 32 + lane;
-  const int64_t r0 = (int64_t)blockIdx.y * kSumRows, r1 = min(n, r0 + kSumRows);
+  const int d = blockIdx.y * 32 + lane;
+  const int64_t r0 = (int64_t)blockIdx.x * kSumRows, r1 = min(n, r0 + kSumRows);
   float s = 0.0f;
   if (d < width) {
 #pragma unroll 8
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(32 * kSumGroups)
   __syncthreads();
   if (group != 0 || d >= width) return;
   for (int k = 1; k < kSumGroups; ++k) s += part[k][lane];
-  if (lam == nullptr) out[(int64_t)blockIdx.y * width + d] = s;
+  if (lam == nullptr) out[(int64_t)blockIdx.x * width + d] = s;
   else if (d < D) out[d] = -c * gs_sigmoid(lam[d]) * s;
 }
 
@@ -546,7 +546,7 @@ template <typename T> cudaError_t backward(const GatedScanBackwardArgs &b) {
     const int64_t m = ceil_div(n, kSumRows);
     const bool last = m == 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ceil_div(width, 32), (unsigned)m, 1);
+    cfg.gridDim = dim3((unsigned)m, (unsigned)ceil_div(width, 32), 1);
     cfg.blockDim = dim3(32 * kSumGroups, 1, 1);
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[1];

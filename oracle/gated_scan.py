@@ -11,8 +11,10 @@ factor that enters a product is taken to be off by KAPPA half-steps of fp32, and
 recurrences carry those errors on, over the magnitudes (absolute sums, so that
 cancellation is covered).  KAPPA: the argument of sigmoid's exponential is off by
 half a step of |r| <= 8, the exponential, the sum and the quotient by one or two
-steps each (|r| + 5); la and a add four and m, a square root, halves what it is
-given; b = m G x has two such factors, and three products: 2 * 13 + 3 < 32.
+steps each (|r| + 5); la adds two and m, a square root, halves what it is given;
+b = m G x has two such factors, and three products: 2 * 13 + 3 < 32.  a = exp(la)
+turns la's relative error, |r| + 7 < 16 half-steps, into one of |la| times that, and
+adds two steps of its own: KAPPA (1 + |la|) in all.
 """
 from __future__ import annotations
 
@@ -45,8 +47,9 @@ def forward(lam, x, r, g, z=None, h0=None, c=8.0):
     M, E = np.abs(h), np.zeros(D)
     for t in range(L):
         h = a[t] * h + b[t]
-        M = a[t] * M + np.abs(b[t])
-        E = a[t] * E + KAPPA * U * M
+        aM = a[t] * M
+        M = aM + np.abs(b[t])
+        E = a[t] * E + KAPPA * U * (M - la[t] * aM)
         hs[t], size[t], off[t] = h, M, E
     out = {"h": hs, "h_end": h, "size": size, "h_off": off, "h_end_off": E}
     if z is None:
@@ -85,7 +88,8 @@ def backward(lam, x, r, g, dy, z=None, h0=None, dh=None, c=8.0):
         d[t] = ds[t] + e
         dM[t] = np.abs(ds[t]) + eM
         dE[t] = eE + KAPPA * U * dM[t]
-        e, eM, eE = a[t] * d[t], a[t] * dM[t], a[t] * (dE[t] + KAPPA * U * dM[t])
+        e, eM = a[t] * d[t], a[t] * dM[t]
+        eE = a[t] * (dE[t] + KAPPA * U * (1.0 - la[t]) * dM[t])
     out["h0"], out["h0_off"] = e, eE
     out["x"], out["x_off"] = d * m * G, m * G * (dE + KAPPA * U * dM)
     out["g"] = d * m * x * G * (1.0 - G)
@@ -93,7 +97,7 @@ def backward(lam, x, r, g, dy, z=None, h0=None, dh=None, c=8.0):
     out["g_off"] = m * np.abs(x) * G * ((1.0 - G) * (dE + KAPPA * U * dM) + KAPPA * U * dM)
     per_m = np.where(m > 0, 1.0 / np.where(m > 0, m, 1.0), 0.0)
     k = a * hp - a * a * per_m * G * x
-    k_size = a * hp_size + a * a * per_m * G * np.abs(x)
+    k_size = a * (1.0 - la) * hp_size + a * a * (1.0 - la) * per_m * G * np.abs(x)
     dla = d * k
     dla_off = dE * k_size + dM * (a * hp_off + 2 * KAPPA * U * k_size)
     out["r"] = dla * la * (1.0 - R)

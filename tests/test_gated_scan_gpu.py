@@ -158,6 +158,29 @@ def test_wide_gates_and_decays(dtype):
     _compare(v, [200, 200], dtype, False, h0, dh, y, h, gr)
 
 
+@pytest.mark.parametrize("dtype,gated", [("f32", False), ("bf16", True)])
+def test_wide_decays_in_packed_rows(dtype, gated):
+    D, lens = 72, [3, 400, 1, 0, 130, 129, 16]
+    lam = torch.linspace(-30, 12, D)
+    v = _inputs(None, sum(lens), D, 50, dtype, gated, spread=4.0, lam=lam)
+    h0, dh = _states(len(lens), D, 51)
+    y, h, gr = _run(v, lens, D, dtype, True, h0, dh)
+    _compare(v, lens, dtype, True, h0, dh, y, h, gr)
+
+
+@pytest.mark.parametrize("dtype,gated,lo", [("f32", True, -5.0), ("bf16", False, -5.0),
+                                            ("bf16", True, 3.0)])
+@pytest.mark.parametrize("L", [17, 64])
+def test_short_rows_of_a_large_batch(L, dtype, gated, lo):
+    # enough threads for a row each; decays near one and far from it
+    D, batch = 1096, 120
+    lam = lo + torch.rand(D, generator=torch.Generator().manual_seed(1))
+    v = _inputs(batch, L, D, 52, dtype, gated, lam=lam)
+    h0, dh = _states(batch, D, 53)
+    y, h, gr = _run(v, [L] * batch, D, dtype, False, h0, dh)
+    _compare(v, [L] * batch, dtype, False, h0, dh, y, h, gr)
+
+
 def test_shut_gates_keep_the_state_exactly():
     # r = -inf at padded tokens: the state passes through, nothing is NaN, forwards and back
     D, L = 40, 300
@@ -455,6 +478,14 @@ def test_nan_of_any_payload():
         assert torch.isnan(gr["h_state"]).all() if k in ("dh", "dy", "r", "lam") else True
         if k in ("x", "r", "g", "h0", "lam"):
             assert torch.isnan(y).all() and torch.isnan(h).all(), k
+
+
+def test_sums_over_many_partial_ones():
+    # lam's gradient over more tiles than one round of its sum takes
+    D, batch = 8, 1500
+    v = _inputs(batch, 20, D, 54, "f32", False)
+    y, h, gr = _run(v, [20] * batch, D, "f32", False, None, None)
+    _compare(v, [20] * batch, "f32", False, None, None, y, h, gr)
 
 
 def test_a_long_row():
