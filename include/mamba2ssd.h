@@ -372,6 +372,8 @@ MAMBA2_API int mamba2_conv_ssd_prefill_backward(
 /* Tokens of a checkpoint (see mamba2_gated_scan_prefill). */
 #define MAMBA2_GATED_SCAN_CHUNK 16
 
+/* Limits (MAMBA2_ERR_UNSUPPORTED beyond): batch < 2^29, L < 2^31 and, with rows =
+ * batch, or 1 for packed rows, rows * ceil(L / 64) * ceil(D / 32) < 2^30. */
 typedef struct {
   int64_t batch;     /* b >= 0: sequences */
   int64_t seqlen;    /* L >= 0: tokens of each, or of all of them in packed rows; step: ignored */

@@ -677,20 +677,20 @@ MAMBA2_API int mamba2_conv_ssd_prefill_backward(
 namespace m2 {
 namespace {
 
-int gated_scan_dims_status(const mamba2_gated_scan_dims *d) {
+int64_t gated_scan_rows(const mamba2_gated_scan_dims *d, bool packed) {
+  return packed ? (d->seqlen > 0 ? 1 : 0) : d->batch;
+}
+
+int gated_scan_dims_status(const mamba2_gated_scan_dims *d, bool packed) {
   if (d == nullptr || d->batch < 0 || d->seqlen < 0 || d->width < 1) return MAMBA2_ERR_INVALID_ARG;
   if (d->io_dtype != MAMBA2_F32 && d->io_dtype != MAMBA2_BF16) return MAMBA2_ERR_INVALID_ARG;
   if (!(d->decay_scale > 0.0f) || !std::isfinite(d->decay_scale)) return MAMBA2_ERR_INVALID_ARG;
   if (d->width % 8 != 0 || d->width > (1 << 20)) return MAMBA2_ERR_UNSUPPORTED;
   // tokens, sequences (in packed rows beside two bits) and tiles are counted in 32 bits
-  if (d->batch >= (int64_t)1 << 29 || d->seqlen >= (int64_t)1 << 31 ||
-      gs_tiles(d->batch, std::max<int64_t>(d->seqlen, 1), d->width) >= (int64_t)1 << 30)
-    return MAMBA2_ERR_UNSUPPORTED;
+  if (d->batch >= (int64_t)1 << 29 || d->seqlen >= (int64_t)1 << 31) return MAMBA2_ERR_UNSUPPORTED;
+  const int64_t of_row = gs_tiles(std::max<int64_t>(d->seqlen, 1), d->width);  // <= 2^40
+  if (gated_scan_rows(d, packed) > (((int64_t)1 << 30) - 1) / of_row) return MAMBA2_ERR_UNSUPPORTED;
   return MAMBA2_OK;
-}
-
-int64_t gated_scan_rows(const mamba2_gated_scan_dims *d, bool packed) {
-  return packed ? (d->seqlen > 0 ? 1 : 0) : d->batch;
 }
 
 bool rows_ok(const void *p, int64_t ld, int64_t width) {
@@ -700,8 +700,9 @@ bool rows_ok(const void *p, int64_t ld, int64_t width) {
 // The inputs shared by prefill, step and backward.
 int gated_scan_inputs(const mamba2_gated_scan_dims *d, const float *lam, const void *x,
                       int64_t ld_x, const void *r, int64_t ld_r, const void *g, int64_t ld_g,
-                      const void *z, int64_t ld_z, bool tokens, GatedScanArgs *a) {
-  const int st = gated_scan_dims_status(d);
+                      const void *z, int64_t ld_z, bool packed, bool tokens,
+                      GatedScanArgs *a) {
+  const int st = gated_scan_dims_status(d, packed);
   if (st != MAMBA2_OK) return st;
   if (lam == nullptr || !aligned(lam, 4)) return MAMBA2_ERR_INVALID_ARG;
   if (tokens && (!rows_ok(x, ld_x, d->width) || !rows_ok(r, ld_r, d->width) ||
@@ -729,21 +730,21 @@ int gated_scan_inputs(const mamba2_gated_scan_dims *d, const float *lam, const v
 
 MAMBA2_API size_t mamba2_gated_scan_workspace_size(const mamba2_gated_scan_dims *dims,
                                                    int packed) {
-  if (gated_scan_dims_status(dims) != MAMBA2_OK) return 0;
+  if (gated_scan_dims_status(dims, packed != 0) != MAMBA2_OK) return 0;
   return gated_scan_workspace(gated_scan_rows(dims, packed != 0), dims->seqlen, dims->width,
                               dims->io_dtype, packed != 0);
 }
 
 MAMBA2_API size_t mamba2_gated_scan_backward_workspace_size(const mamba2_gated_scan_dims *dims,
                                                             int packed) {
-  if (gated_scan_dims_status(dims) != MAMBA2_OK) return 0;
+  if (gated_scan_dims_status(dims, packed != 0) != MAMBA2_OK) return 0;
   return gated_scan_backward_workspace(gated_scan_rows(dims, packed != 0), dims->seqlen,
                                        dims->width, dims->io_dtype, packed != 0);
 }
 
 MAMBA2_API size_t mamba2_gated_scan_checkpoint_count(const mamba2_gated_scan_dims *dims,
                                                      int packed) {
-  if (gated_scan_dims_status(dims) != MAMBA2_OK) return 0;
+  if (gated_scan_dims_status(dims, packed != 0) != MAMBA2_OK) return 0;
   return (size_t)gated_scan_rows(dims, packed != 0) * (size_t)ceil_div(dims->seqlen, kGsChunk) *
          (size_t)dims->width;
 }
@@ -757,7 +758,7 @@ MAMBA2_API int mamba2_gated_scan_prefill(
   GatedScanArgs a;
   const bool tokens = dims != nullptr && dims->seqlen > 0 && (dims->batch > 0 || cu_seqlens);
   const int st = gated_scan_inputs(dims, lam, x, x_row_stride, r, r_row_stride, g, g_row_stride, z,
-                                   z_row_stride, tokens, &a);
+                                   z_row_stride, cu_seqlens != nullptr, tokens, &a);
   if (st != MAMBA2_OK) return st;
   if (states_in != 0 && states_in != 1) return MAMBA2_ERR_INVALID_ARG;
   if ((states_in && h_state == nullptr) || !aligned(h_state, 16) || !aligned(checkpoints, 16) ||
@@ -799,7 +800,7 @@ MAMBA2_API int mamba2_gated_scan_step(const mamba2_gated_scan_dims *dims, const 
   d.seqlen = 1;
   if (d.batch > (int64_t)65535 * 8) return MAMBA2_ERR_UNSUPPORTED;  // grid limit
   const int st = gated_scan_inputs(&d, lam, x, x_row_stride, r, r_row_stride, g, g_row_stride, z,
-                                   z_row_stride, d.batch > 0, &a);
+                                   z_row_stride, false, d.batch > 0, &a);
   if (st != MAMBA2_OK) return st;
   if (d.batch == 0) return MAMBA2_OK;
   if (y == nullptr || !aligned(y, 16) || h_state == nullptr || !aligned(h_state, 16))
@@ -824,7 +825,7 @@ MAMBA2_API int mamba2_gated_scan_backward(
   GatedScanBackwardArgs b;
   const bool tokens = dims != nullptr && dims->seqlen > 0 && (dims->batch > 0 || cu_seqlens);
   const int st = gated_scan_inputs(dims, lam, x, x_row_stride, r, r_row_stride, g, g_row_stride, z,
-                                   z_row_stride, tokens, &b.f);
+                                   z_row_stride, cu_seqlens != nullptr, tokens, &b.f);
   if (st != MAMBA2_OK) return st;
   if (d_lam == nullptr || !aligned(d_lam, 4) || !aligned(h_state_in, 16) ||
       !aligned(d_h_state_out, 16) || !aligned(d_h_state_in, 16) || !aligned(checkpoints, 16) ||

@@ -55,10 +55,8 @@ cudaError_t take_gated_scan_errors(unsigned int *out);
 cudaError_t set_gated_scan_stall(unsigned int v);
 cudaError_t take_gated_scan_backward_errors(unsigned int *out);
 cudaError_t set_gated_scan_backward_stall(unsigned int v);
-// Tiles of 64 tokens and 32 channels in a call: they are counted in 32 bits.
-inline int64_t gs_tiles(int64_t rows, int64_t L, int64_t D) {
-  return rows * ceil_div(L, 64) * ceil_div(D, 32);
-}
+// Tiles of 64 tokens and 32 channels in a row: those of a call are counted in 32 bits.
+inline int64_t gs_tiles(int64_t L, int64_t D) { return ceil_div(L, 64) * ceil_div(D, 32); }
 
 // ---------------------------------------------------------------- arithmetic
 __device__ __forceinline__ float gs_sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }

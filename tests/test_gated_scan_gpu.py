@@ -513,6 +513,29 @@ def test_more_sequences_than_65535():
            "dh0")
 
 
+@pytest.mark.parametrize("dtype,gated", [("f32", False), ("bf16", True)])
+def test_sequences_times_tokens_beyond_the_tiles(dtype, gated):
+    # as one packed row they are few tiles, as rows of all tokens they would pass 2^30
+    D, n = 64, 200000
+    assert n * (n // 64) * (D // 32) >= 1 << 30
+    v = _inputs(None, n, D, 48, dtype, gated)
+    h0, dh = _states(n, D, 49)
+    y, h, gr = _run(v, [1] * n, D, dtype, True, h0, dh)
+    # single tokens: one token of n * D channels
+    lam = np.tile(_np(v["lam"]), n)
+    one = lambda t: None if t is None else _np(t).reshape(1, -1)
+    ins = [one(v[k]) for k in ("x", "r", "g")]
+    f = GS.forward(lam, *ins, one(v["z"]), one(h0)[0], C)
+    bf = dtype == "bf16"
+    _check(y.reshape(1, -1), f["y"], f["y_off"], "y", bf)
+    _check(h.reshape(-1), f["h_end"], f["h_end_off"], "h")
+    b = GS.backward(lam, *ins, one(v["dy"]), one(v["z"]), one(h0)[0], one(dh)[0], C)
+    for k in ("x", "r", "g") + (("z",) if gated else ()):
+        _check(gr[k].reshape(1, -1), b[k], b[k + "_off"], f"d{k}", bf)
+    _check(gr["h_state"].reshape(-1), b["h0"], b["h0_off"], "dh0")
+    _check(gr["lam"], b["lam"].reshape(n, D).sum(0), b["lam_off"].reshape(n, D).sum(0), "dlam")
+
+
 def test_waits_that_run_out_are_reported():
     D, L = 200, 900
     v = _inputs(2, L, D, 48, "bf16", True)

@@ -61,6 +61,30 @@ def test_bad_dims(kw, want):
         assert m2.lib().mamba2_gated_scan_checkpoint_count(ctypes.byref(d), packed) == 0
 
 
+def test_limits_count_rows_not_sequences():
+    # 4096 sequences in a packed row of 131072 tokens are one row of tiles
+    d = _dims(batch=4096, seqlen=131072, width=5120)
+    sizes = (m2.mamba2_gated_scan_workspace_size, m2.mamba2_gated_scan_backward_workspace_size)
+    for f in sizes:
+        assert f(d, True) > 0 and f(d, False) == 0
+    assert m2.lib().mamba2_gated_scan_checkpoint_count(ctypes.byref(d), 1) == 8192 * 5120
+    ld = dict(lx=5120, lr=5120, lg=5120)
+    assert _prefill(d, cu=A0 + 0x9000, bytes=0, **ld) == WORKSPACE
+    assert _backward(d, cu=A0 + 0x9000, bytes=0, **ld) == WORKSPACE
+    assert _prefill(d, **ld) == UNSUPPORTED and _backward(d, **ld) == UNSUPPORTED
+    # the most tiles, and one more
+    most = _dims(batch=(1 << 30) - 1, seqlen=1, width=32)
+    assert sizes[0](most) == 0  # (sequences are fewer than 2^29)
+    for batch, ok in (((1 << 29) - 1, True), (1 << 29, False)):
+        assert (sizes[0](_dims(batch=batch, seqlen=64, width=64)) > 0) == ok
+    for seqlen, ok in (((1 << 31) - 128, True), ((1 << 31) - 1, False)):
+        assert (sizes[0](_dims(batch=1, seqlen=seqlen, width=1024)) > 0) == ok
+    # products that pass 64 bits
+    d = _dims(batch=1 << 28, seqlen=(1 << 31) - 64, width=1 << 20)
+    assert sizes[0](d) == 0 and sizes[1](d) == 0
+    assert _prefill(d, lx=1 << 20, lr=1 << 20, lg=1 << 20) == UNSUPPORTED
+
+
 def test_sizes():
     assert m2.lib().mamba2_gated_scan_checkpoint_count(ctypes.byref(_dims()), 0) == 2 * 19 * 64
     assert m2.lib().mamba2_gated_scan_checkpoint_count(ctypes.byref(_dims()), 1) == 19 * 64
