@@ -197,8 +197,9 @@ template <typename T> struct In {
 constexpr int kShortBatch = 4;
 template <typename T, bool GATED>
 __global__ void __launch_bounds__(128, 5)
-    gs_short_kernel(In<T> in, const float *__restrict__ lam, float c, int64_t pairs, int L, int D,
-                    const float *h_in, float *h_out, float *__restrict__ ck, T *__restrict__ y) {
+    gs_short_kernel(In<T> in, const float *lam, float c, int64_t pairs, int L, int D,
+                    const float *h_in, float *h_out, float *ck, T *y) {
+  grid_dependency_wait();
   using V = typename Pair<T>::V;
   const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (at >= pairs) return;
@@ -274,8 +275,9 @@ template <typename T> struct Lane {
 constexpr int kStepGroups = 64, kStepRows = 4, kStepTurns = 2;
 template <typename T, bool GATED>
 __global__ void __launch_bounds__(kStepGroups *kStepRows)
-    gs_step_kernel(In<T> in, const float *__restrict__ lam, float c, int64_t batch, int D,
-                   float *__restrict__ h, T *__restrict__ y) {
+    gs_step_kernel(In<T> in, const float *lam, float c, int64_t batch, int D,
+                   float *h, T *y) {
+  grid_dependency_wait();
   constexpr int V = Lane<T>::V;
   __shared__ float ncs[kStepGroups * V];
   const int group = threadIdx.x % kStepGroups, c0 = blockIdx.x * kStepGroups * V;
@@ -356,10 +358,9 @@ template <typename T> cudaError_t prefill(const GatedScanArgs &a) {
   if (a.cu == nullptr && (a.L <= kShort || (a.L <= kShortOfMany && pairs >= kMany))) {
     const auto kernel = a.z != nullptr && a.y != nullptr ? gs_short_kernel<T, true>
                                                          : gs_short_kernel<T, false>;
-    kernel<<<(unsigned)ceil_div(pairs, 128), 128, 0, a.stream>>>(
-        inputs<T>(a), a.lam, a.c, pairs, (int)a.L, a.D, a.states_in ? a.h : nullptr,
-        a.no_state_out ? nullptr : a.h, a.ck, static_cast<T *>(a.y));
-    return cudaGetLastError();
+    return launch_dependent(kernel, (unsigned)ceil_div(pairs, 128), 128, 0, a.stream, inputs<T>(a), a.lam,
+                            a.c, pairs, (int)a.L, a.D, a.states_in ? a.h : (float *)nullptr,
+                            a.no_state_out ? (float *)nullptr : a.h, a.ck, static_cast<T *>(a.y));
   }
   const bool packed = a.cu != nullptr, gated = a.z != nullptr && a.y != nullptr;
   const Plan w = plan_of(rows, a.L, a.D, Tiles<T, false>::kTile, packed);
@@ -384,9 +385,8 @@ template <typename T> cudaError_t step(const GatedScanArgs &a) {
   const dim3 grid((unsigned)ceil_div(a.D, kStepGroups * Lane<T>::V),
                   (unsigned)ceil_div(a.batch, kStepRows * kStepTurns));
   const auto kernel = a.z != nullptr ? gs_step_kernel<T, true> : gs_step_kernel<T, false>;
-  kernel<<<grid, kStepGroups * kStepRows, 0, a.stream>>>(inputs<T>(a), a.lam, a.c, a.batch, a.D,
-                                                         a.h, static_cast<T *>(a.y));
-  return cudaGetLastError();
+  return launch_dependent(kernel, grid, kStepGroups * kStepRows, 0, a.stream, inputs<T>(a), a.lam,
+                          a.c, a.batch, a.D, a.h, static_cast<T *>(a.y));
 }
 
 }  // namespace

@@ -94,6 +94,7 @@ __global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, uin
                                int64_t L, int *marks, unsigned int *bad,
                                const float *empty_in, float *empty_out) {
   launch_dependents();
+  grid_dependency_wait();
   const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t all = (int64_t)gridDim.x * blockDim.x;
   for (int64_t i = at; i < (D + 63) / 64 * 64; i += all)
@@ -142,7 +143,7 @@ __device__ __forceinline__ void entered_signal(int half) {
 
 // A block's start: false if there is nothing to do.
 template <typename S, bool PACKED> __device__ __forceinline__ bool begin(S &sm, const Scan &p) {
-  if (test_stall(&g_gs_stall, &g_gs_errors)) return false;
+  const bool stalled = test_stall(&g_gs_stall, &g_gs_errors);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) mbar_init(&sm.full[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&sm.segs[s], kWarps);
@@ -150,8 +151,9 @@ template <typename S, bool PACKED> __device__ __forceinline__ bool begin(S &sm, 
     fence_mbar_init();
   }
   __syncthreads();
+  // (every block waits, so that what waits for this kernel has waited for the one before)
   grid_dependency_wait();
-  return !(PACKED && *p.bad);
+  return !(stalled || (PACKED && *p.bad));
 }
 
 // The segments before `seg` (in the order of the scan) as one map.
@@ -347,6 +349,37 @@ inline Plan plan_of(int64_t rows, int64_t L, int D, int tile_tokens, bool packed
   return p;
 }
 
+// Launches a kernel whose blocks may start while the one before drains (they wait for it; so
+// none of its pointers may be __restrict__, which lets them be read before).  The first
+// kernel of a call too: 2 us less for calls in turn, prefill 46.3 against 44.3 us at 4096
+// tokens of 5120 channels.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), ContextOnce &once, unsigned grid, int threads,
+                             size_t smem, cudaStream_t stream, A... args) {
+  if (!once.done()) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    once.set();
+  }
+  return launch_dependent(kernel, grid, threads, smem, stream, args...);
+}
+
 // The parameters of a scan over `a`'s rows whose workspace is at ws, and the launch that
 // prepares it.
 inline cudaError_t prepare(const GatedScanArgs &a, const Plan &w, char *ws, const float *first,
@@ -370,11 +403,11 @@ inline cudaError_t prepare(const GatedScanArgs &a, const Plan &w, char *ws, cons
   p->states = reinterpret_cast<float2 *>(ws + w.states);
   const int64_t nrecords = (int64_t)(w.marks - w.maps) / 16;  // maps and states, side by side
   const int64_t work = std::max(std::max<int64_t>(a.D, nrecords), packed ? a.L : 0);
-  gs_prep_kernel<<<(unsigned)std::min<int64_t>(ceil_div(work, 256), 148 * 4), 256, 0, a.stream>>>(
-      a.lam, a.c, a.D, const_cast<float *>(p->ncs), reinterpret_cast<uint4 *>(ws + w.maps),
-      nrecords, p->ticket, a.cu, a.batch, a.L, const_cast<int *>(p->marks),
-      const_cast<unsigned int *>(p->bad), empty_in, empty_out);
-  return cudaGetLastError();
+  return launch_dependent(gs_prep_kernel, (unsigned)std::min<int64_t>(ceil_div(work, 256), 148 * 4), 256, 0,
+                          a.stream, a.lam, a.c, a.D, const_cast<float *>(p->ncs),
+                          reinterpret_cast<uint4 *>(ws + w.maps), nrecords, p->ticket, a.cu, a.batch,
+                          a.L, const_cast<int *>(p->marks), const_cast<unsigned int *>(p->bad),
+                          empty_in, empty_out);
 }
 
 inline int sm_count() {
@@ -387,29 +420,6 @@ inline int sm_count() {
     known[dev].store(n, std::memory_order_relaxed);
   }
   return n;
-}
-
-// Launches a kernel whose blocks may start while the one before drains (they wait for it).
-template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kernel)(P...), ContextOnce &once, int64_t grid, int threads,
-                             size_t smem, cudaStream_t stream, A... args) {
-  if (!once.done()) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    once.set();
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3((unsigned)threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace

@@ -7,10 +7,10 @@
 // nearest, ties to even), and a state that was read back and is written again
 // gives the same values.
 //
-// Bytes bound both ways.  256 SSM states of 80 x 64 x 64 in fp32 (336 MB) into int8: 76 us,
-// 5.5 TB/s; back: 69 us, 6.1 TB/s.  bf16: 48 and 44 us.  What a store lacks to the copy rate
+// Bytes bound both ways.  256 SSM states of 80 x 64 x 64 in fp32 (336 MB) into int8: 73 us,
+// 5.7 TB/s; back: 67 us, 6.3 TB/s.  bf16: 46 and 41 us.  What a store lacks to the copy rate
 // is the maximum that each block's values wait for, and the search for a later row of the
-// same slot.
+// same slot.  (2 us of each less than with launches that begin where the kernel before ends.)
 #include <cuda_fp8.h>
 
 #include "state_cache.cuh"
@@ -141,11 +141,14 @@ template <> struct Vec<__nv_bfloat16> {
 // Rows on 16-byte boundaries: a lane takes 16 bytes of the state, LANES lanes a
 // block of LANES * V values; a warp has kU such pieces of 32 * V values under way.
 constexpr int kU = 4;
+// (No pointer is __restrict__: what nobody else changes may be read before the wait for
+// the kernel that makes it.)
 template <typename T, bool INT8, int LANES>
 __global__ void __launch_bounds__(kThreads)
-    store_vec_kernel(const T *__restrict__ state, int64_t ld, int64_t n, int64_t nb,
-                     const int32_t *__restrict__ slots, int64_t batch, int64_t nslots,
-                     uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+    store_vec_kernel(const T *state, int64_t ld, int64_t n, int64_t nb,
+                     const int32_t *slots, int64_t batch, int64_t nslots,
+                     uint8_t *codes, uint8_t *scales) {
+  grid_dependency_wait();
   constexpr int V = Vec<T>::V;
   const int64_t b = blockIdx.y;
   const int lane = threadIdx.x & 31;
@@ -183,9 +186,10 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T, bool INT8>
 __global__ void __launch_bounds__(kThreads)
-    load_vec_kernel(T *__restrict__ state, int64_t ld, int64_t n, int shift, int64_t nb,
-                    const int32_t *__restrict__ slots, int64_t nslots,
-                    const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales) {
+    load_vec_kernel(T *state, int64_t ld, int64_t n, int shift, int64_t nb,
+                    const int32_t *slots, int64_t nslots,
+                    const uint8_t *codes, const uint8_t *scales) {
+  grid_dependency_wait();
   constexpr int V = Vec<T>::V;
   const int64_t b = blockIdx.y;
   const int64_t s = slot_of(slots, b, nslots);
@@ -219,17 +223,18 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Rows anywhere (a row of 327679 values: stores 109 us fp32, 112 us bf16, loads 112 us, with
-// the 16-byte lanes of the same sizes at 76, 48 and 69): a lane takes single values, 32 apart, so that a warp's loads and
+// Rows anywhere (a row of 327679 values: stores 107 us fp32, 110 us bf16, loads 100 us, with
+// the 16-byte lanes of the same sizes at 73, 46 and 67): a lane takes single values, 32 apart, so that a warp's loads and
 // stores are of neighbouring ones; a warp has kPer * 32 values (whole blocks) under
 // way.
 constexpr int kPer = 8;
 
 template <typename T, bool INT8, int PER>  // PER: a block's values in a lane
 __global__ void __launch_bounds__(kThreads)
-    store_any_kernel(const T *__restrict__ state, int64_t ld, int64_t n, int64_t nb,
-                     const int32_t *__restrict__ slots, int64_t batch, int64_t nslots,
-                     uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+    store_any_kernel(const T *state, int64_t ld, int64_t n, int64_t nb,
+                     const int32_t *slots, int64_t batch, int64_t nslots,
+                     uint8_t *codes, uint8_t *scales) {
+  grid_dependency_wait();
   const int64_t b = blockIdx.y;
   const int lane = threadIdx.x & 31;
   const int64_t i0 =
@@ -259,9 +264,10 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T, bool INT8>
 __global__ void __launch_bounds__(kThreads)
-    load_any_kernel(T *__restrict__ state, int64_t ld, int64_t n, int shift, int64_t nb,
-                    const int32_t *__restrict__ slots, int64_t nslots,
-                    const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales) {
+    load_any_kernel(T *state, int64_t ld, int64_t n, int shift, int64_t nb,
+                    const int32_t *slots, int64_t nslots,
+                    const uint8_t *codes, const uint8_t *scales) {
+  grid_dependency_wait();
   const int64_t b = blockIdx.y;
   const int64_t s = slot_of(slots, b, nslots);
   if (s < 0) return;
@@ -283,6 +289,21 @@ __global__ void __launch_bounds__(kThreads)
     if (32 * u < left) out[32 * u] = from_f<T>(decode1<INT8>(q[u], scale_of(e[u])));
 }
 
+// A launch that is made ready while the kernel before it ends (it waits for that one).
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // Whether every row of the state is on a 16-byte boundary and its codes can be
@@ -301,24 +322,19 @@ template <typename T, bool INT8> cudaError_t store(const StateCacheArgs &a) {
   uint8_t *codes = static_cast<uint8_t *>(a.codes);
   if (on_boundaries<T>(a)) {
     const dim3 grid((unsigned)ceil_div(a.n, (int64_t)kThreads * V * kU), (unsigned)a.batch);
-#define M2_STORE(block)                                                                      \
-  store_vec_kernel<T, INT8, block / V><<<grid, kThreads, 0, a.stream>>>(                     \
-      state, a.ld, a.n, nb, a.slots, a.batch, a.nslots, codes, a.scales)
-    if (a.block == 32) M2_STORE(32);
-    else if (a.block == 64) M2_STORE(64);
-    else M2_STORE(128);
-#undef M2_STORE
+    const auto kernel = a.block == 32   ? store_vec_kernel<T, INT8, 32 / V>
+                        : a.block == 64 ? store_vec_kernel<T, INT8, 64 / V>
+                                        : store_vec_kernel<T, INT8, 128 / V>;
+    return launch(kernel, grid, a.stream, state, a.ld, a.n, nb, a.slots, a.batch, a.nslots, codes,
+                  a.scales);
   } else {
     const dim3 grid((unsigned)ceil_div(a.n, kThreads * kPer), (unsigned)a.batch);
-#define M2_STORE(block)                                                                      \
-  store_any_kernel<T, INT8, block / 32><<<grid, kThreads, 0, a.stream>>>(                    \
-      state, a.ld, a.n, nb, a.slots, a.batch, a.nslots, codes, a.scales)
-    if (a.block == 32) M2_STORE(32);
-    else if (a.block == 64) M2_STORE(64);
-    else M2_STORE(128);
-#undef M2_STORE
+    const auto kernel = a.block == 32   ? store_any_kernel<T, INT8, 1>
+                        : a.block == 64 ? store_any_kernel<T, INT8, 2>
+                                        : store_any_kernel<T, INT8, 4>;
+    return launch(kernel, grid, a.stream, state, a.ld, a.n, nb, a.slots, a.batch, a.nslots, codes,
+                  a.scales);
   }
-  return cudaGetLastError();
 }
 template <typename T, bool INT8> cudaError_t load(const StateCacheArgs &a) {
   constexpr int V = Vec<T>::V;
@@ -326,15 +342,14 @@ template <typename T, bool INT8> cudaError_t load(const StateCacheArgs &a) {
   T *state = static_cast<T *>(a.state);
   const uint8_t *codes = static_cast<const uint8_t *>(a.codes);
   if (on_boundaries<T>(a))
-    load_vec_kernel<T, INT8>
-        <<<dim3((unsigned)ceil_div(a.n, (int64_t)kThreads * V * kU), (unsigned)a.batch), kThreads,
-           0, a.stream>>>(state, a.ld, a.n, log2_of(a.block), nb, a.slots, a.nslots, codes,
-                          a.scales);
-  else
-    load_any_kernel<T, INT8>
-        <<<dim3((unsigned)ceil_div(a.n, kThreads * kPer), (unsigned)a.batch), kThreads, 0,
-           a.stream>>>(state, a.ld, a.n, log2_of(a.block), nb, a.slots, a.nslots, codes, a.scales);
-  return cudaGetLastError();
+    return launch(load_vec_kernel<T, INT8>,
+                  dim3((unsigned)ceil_div(a.n, (int64_t)kThreads * V * kU), (unsigned)a.batch),
+                  a.stream, state, a.ld, a.n, log2_of(a.block), nb, a.slots, a.nslots, codes,
+                  static_cast<const uint8_t *>(a.scales));
+  return launch(load_any_kernel<T, INT8>,
+                dim3((unsigned)ceil_div(a.n, kThreads * kPer), (unsigned)a.batch), a.stream, state,
+                a.ld, a.n, log2_of(a.block), nb, a.slots, a.nslots, codes,
+                static_cast<const uint8_t *>(a.scales));
 }
 
 }  // namespace
