@@ -593,3 +593,41 @@ def test_binding_refuses_what_does_not_fit():
         w = 12
         m2.gated_scan_prefill(m2.make_gated_scan_dims(2, L, w), torch.zeros(w, device="cuda"),
                               *[torch.zeros(2, L, w, device="cuda", dtype=torch.bfloat16)] * 3)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_many_tiles_a_step_match_oracle(dtype, gated):
+    # 24 tiles of a step and more: states are put together from the one eight tiles back
+    batch, L, D = 8, 3000, 136
+    v = _inputs(batch, L, D, 60, dtype, gated)
+    h0, dh = _states(batch, D, 61)
+    y, h, gr = _run(v, [L] * batch, D, dtype, False, h0, dh)
+    _compare(v, [L] * batch, dtype, False, h0, dh, y, h, gr)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("lens", [[3000], [1300, 0, 1, 1500, 199]], ids=["one", "five"])
+def test_many_tiles_a_step_of_packed_rows_match_oracle(lens, dtype, gated):
+    D = 800
+    v = _inputs(None, sum(lens), D, 62, dtype, gated)
+    h0, dh = _states(len(lens), D, 63)
+    y, h, gr = _run(v, lens, D, dtype, True, h0, dh)
+    _compare(v, lens, dtype, True, h0, dh, y, h, gr)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_the_same_bits_from_eight_tiles_back_and_from_further(dtype, gated):
+    # nine rows look eight tiles back, one row of them 32: bit for bit the same
+    D, L, batch = 72, 2600, 9
+    v = _inputs(batch, L, D, 64, dtype, gated)
+    h0, dh = _states(batch, D, 65)
+    y, h, gr = _run(v, [L] * batch, D, dtype, False, h0, dh)
+    for i in (0, 4, 8):
+        one = {k: (t if t is None or k == "lam" else t[i:i + 1].contiguous()) for k, t in v.items()}
+        y1, h1, gr1 = _run(one, [L], D, dtype, False, h0[i:i + 1], dh[i:i + 1])
+        assert torch.equal(y1[0], y[i]) and torch.equal(h1[0], h[i])
+        for k in ("x", "r", "g", "h_state") + (("z",) if gated else ()):
+            assert torch.equal(gr1[k][0], gr[k][i]), k
