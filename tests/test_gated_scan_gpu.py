@@ -4,6 +4,8 @@ Tolerances: an fp32 result may be off by the oracle's own running error bound (e
 factor off by KAPPA half-steps of fp32, carried through the recurrence); a bf16 result by
 that, plus half a step of bf16 (2^-8 of the value).
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -631,3 +633,38 @@ def test_the_same_bits_from_eight_tiles_back_and_from_further(dtype, gated):
         assert torch.equal(y1[0], y[i]) and torch.equal(h1[0], h[i])
         for k in ("x", "r", "g", "h_state") + (("z",) if gated else ()):
             assert torch.equal(gr1[k][0], gr[k][i]), k
+
+
+@pytest.mark.parametrize("recompute", [False, True])
+@pytest.mark.parametrize("cu", [[0, 0, 200, 100, 600], [0, 0, 300, 500, 599], [1, 1, 300, 500, 600]])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_bad_offsets_leave_every_output(cu, dtype, recompute):
+    # (an empty sequence before the wrong offset: its state is written before any tile runs)
+    D, L, n = 40, 600, 4
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    v = _inputs(None, L, D, 66, dtype, True)
+    dims = m2.make_gated_scan_dims(n, L, D, io_dtype=dtype, decay_scale=C)
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    h0, dh = _states(n, D, 67)
+    for states_in in (False, True):
+        h = torch.full((n, D), 5.0, device="cuda")
+        y = torch.full((L, D), 6.0, device="cuda", dtype=dt)
+        ck = m2.gated_scan_checkpoints(dims, True).fill_(7.0)
+        m2.gated_scan_prefill(dims, v["lam"], v["x"], v["r"], v["g"], z=v["z"], h_state=h,
+                              states_in=states_in, cu_seqlens=c, checkpoints=ck, y=y)
+        assert m2.device_errors() == 4
+        assert (h == 5).all() and (y == 6).all() and (ck == 7).all()
+    outs = {k: torch.full((L, D), 8.0, device="cuda", dtype=dt) for k in ("x", "r", "g", "z")}
+    outs["lam"] = torch.full((D,), 8.0, device="cuda")
+    outs["h"] = torch.full((n, D), 8.0, device="cuda")
+    size = m2.mamba2_gated_scan_backward_workspace_size(dims, True)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    rows = [a for k in ("x", "r", "g", "z") for a in (v[k].data_ptr(), v[k].stride(0))]
+    st = m2.lib().mamba2_gated_scan_backward(
+        ctypes.byref(dims), v["lam"].data_ptr(), *rows, c.data_ptr(), h0.data_ptr(),
+        v["dy"].data_ptr(), dh.data_ptr(), None if recompute else ck.data_ptr(),
+        *[outs[k].data_ptr() for k in ("x", "r", "g", "z", "lam", "h")], ws.data_ptr(), size,
+        torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and m2.device_errors() == 4
+    for k, t in outs.items():
+        assert (t == 8).all(), k
