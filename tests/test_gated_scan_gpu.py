@@ -668,3 +668,36 @@ def test_bad_offsets_leave_every_output(cu, dtype, recompute):
     assert st == 0 and m2.device_errors() == 4
     for k, t in outs.items():
         assert (t == 8).all(), k
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("batch,L,D,gated,h,d", [
+    (2, 1, 72, False, True, True), (3, 16, 72, True, False, True), (2, 16, 40, False, True, False),
+    (120, 64, 1096, True, True, False), (120, 33, 1096, False, False, False),
+    (2, 700, 136, False, False, True), (2, 700, 136, True, False, False),
+])
+def test_backward_without_checkpoints(batch, L, D, gated, h, d, dtype):
+    # the scan run again inside the call, short rows among them, with and without each state
+    v = _inputs(batch, L, D, 68, dtype, gated)
+    h0, dh = _states(batch, D, 69)
+    h0, dh = h0 if h else None, dh if d else None
+    y, h1, a = _run(v, [L] * batch, D, dtype, False, h0, dh, checkpoints=True)
+    _, _, b = _run(v, [L] * batch, D, dtype, False, h0, dh, checkpoints=False)
+    assert a.keys() == b.keys()
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+    _compare(v, [L] * batch, dtype, False, h0, dh, y, h1, b)
+
+
+@pytest.mark.parametrize("h,d", [(False, True), (True, False), (False, False)])
+@pytest.mark.parametrize("dtype,gated", [("f32", True), ("bf16", False)])
+def test_packed_backward_without_checkpoints(dtype, gated, h, d):
+    lens, D = [5, 0, 300, 1, 130, 16], 72
+    v = _inputs(None, sum(lens), D, 70, dtype, gated)
+    h0, dh = _states(len(lens), D, 71)
+    h0, dh = h0 if h else None, dh if d else None
+    y, h1, a = _run(v, lens, D, dtype, True, h0, dh, checkpoints=True)
+    _, _, b = _run(v, lens, D, dtype, True, h0, dh, checkpoints=False)
+    for k in a:
+        assert torch.equal(a[k], b[k]), k
+    _compare(v, lens, dtype, True, h0, dh, y, h1, b)
