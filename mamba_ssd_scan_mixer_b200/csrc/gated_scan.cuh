@@ -166,25 +166,32 @@ template <bool NEAR> __device__ __forceinline__ void decay2(F2 t, F2 *a, F2 *les
 // exactly as it was (for c softplus(lam) < 32), and an increment lost is below 4e-9 of
 // x.  The 2^35 that m then lacks is in G.
 struct Coeffs {
-  F2 a, b, t, less, R, G, m;  // (G and m scaled by 2^35 and 2^-35)
+  F2 a, b, t, less, m, er, eg;  // (m scaled by 2^-35); er, eg: e^-r, e^-g
 };
 constexpr float kGateScale = 34359738368.0f;  // 2^35
+struct Gates {
+  F2 R, G;  // (G scaled by 2^35)
+};
+// The gates of e^-r and e^-g; `one` and `down` are 1 and 2^-35.
+__device__ __forceinline__ Gates gates(F2 er, F2 eg, F2 one, F2 down) {
+  const F2 pr = add2(er, one), pg = fma2(eg, down, down);
+  const float2 P = unpack(mul2(pr, pg));
+  const F2 inv = f2(rcp(P.x), rcp(P.y));
+  return Gates{mul2(pg, inv), mul2(pr, inv)};
+}
 template <bool NEAR>
 __device__ __forceinline__ Coeffs coefficients(F2 x, F2 r, F2 g, F2 ncs) {
   constexpr float down = 1.0f / kGateScale, down2 = down * down;
   Coeffs c;
   const float2 er = unpack(mul2(r, f2(-kLog2e))), eg = unpack(mul2(g, f2(-kLog2e)));
-  const F2 pr = add2(f2(ex2(er.x), ex2(er.y)), f2(1.0f));
-  const F2 pg = fma2(f2(ex2(eg.x), ex2(eg.y)), f2(down), f2(down));
-  const float2 P = unpack(mul2(pr, pg));
-  const F2 inv = f2(rcp(P.x), rcp(P.y));
-  c.R = mul2(pg, inv);
-  c.G = mul2(pr, inv);
-  c.t = mul2(ncs, c.R);
+  c.er = f2(ex2(er.x), ex2(er.y));
+  c.eg = f2(ex2(eg.x), ex2(eg.y));
+  const Gates k = gates(c.er, c.eg, f2(1.0f), f2(down));
+  c.t = mul2(ncs, k.R);
   decay2<NEAR>(c.t, &c.a, &c.less);
   const float2 v = unpack(mul2(c.less, fma2(c.a, f2(-down2), f2(-down2))));
   c.m = f2(sqrt_ap(v.x), sqrt_ap(v.y));
-  c.b = mul2(mul2(c.m, c.G), x);
+  c.b = mul2(mul2(c.m, k.G), x);
   return c;
 }
 

@@ -701,3 +701,35 @@ def test_packed_backward_without_checkpoints(dtype, gated, h, d):
     for k in a:
         assert torch.equal(a[k], b[k]), k
     _compare(v, lens, dtype, True, h0, dh, y, h1, b)
+
+
+@pytest.mark.parametrize("lam", [-6.0, -1.0, 2.0], ids=["near", "wide", "wider"])
+def test_gradients_of_saturated_gates(lam):
+    """Gates from nearly shut to fully open: the gradients of r and g go with 1 - R and 1 - G, and
+    are as exact, relative to themselves, as everything else.
+
+    One token from a zero state, so that nothing cancels: dg = dy m x G (1 - G) and
+    dr = -dy (a^2 / m) G x la (1 - R).  In half-steps of fp32, with KAPPA for a factor as in the
+    oracle: m G x has KAPPA; 1 - G = e^-g G has twice |g| (the exponential's argument: the
+    constant and the product) and 8 (the exponential, the sum, the reciprocal and the product), and
+    KAPPA for G.  dr has b = m G x, a^2 by a KAPPA (1 + |la|) each, 1 / (1 - a^2) and la by a KAPPA
+    each, and 1 - R as above.  |la| <= 8 * 2.2.  dx = dy m G has KAPPA."""
+    D, n = 512, 40
+    gen = torch.Generator().manual_seed(72)
+    draw = lambda: (40 * torch.rand(n, 1, D, generator=gen) - 20).cuda()  # noqa: E731
+    r, g = draw(), draw()
+    x = torch.randn(n, 1, D, generator=gen).cuda()
+    dy = torch.randn(n, 1, D, generator=gen).cuda()
+    lam = torch.full((D,), lam).cuda()
+    dims = m2.make_gated_scan_dims(n, 1, D, io_dtype="f32", decay_scale=C)
+    gr = m2.gated_scan_backward(dims, lam, x, r, g, dy)
+    rd, gd, ld, xd, dd = (_np(t) for t in (r, g, lam, x, dy))
+    R, G, la, a, m = GS._gates(ld, rd, gd, C)
+    shut_r, shut_g = 1 / (1 + np.exp(rd)), 1 / (1 + np.exp(gd))  # 1 - R, 1 - G
+    want = {"x": dd * m * G, "g": dd * m * xd * G * shut_g,
+            "r": -dd * a * a / m * G * xd * la * shut_r}
+    K = GS.KAPPA
+    off = {"x": K, "g": 2 * K + 2 * np.abs(gd) + 8,
+           "r": (3 + 2 * (1 - la)) * K + K + 2 * np.abs(rd) + 8}
+    for k, w in want.items():
+        _check(gr[k], w, off[k] * GS.U * np.abs(w) + 1e-37, f"d{k}")
