@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
     }
     const F2 k = f2(ncs.x, ncs.y);
     float4 map;
-    const bool close = __all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f);
+    const bool close = __all_sync(0xffffffffu, near(ncs));
     if (close && n == S::kTile) map = make_maps<S, true, true>(in, k, n - first, a, b);
     else if (close) map = make_maps<S, false, true>(in, k, n - first, a, b);
     else map = make_maps<S, false, false>(in, k, n - first, a, b);
@@ -251,8 +251,7 @@ __global__ void __launch_bounds__(128, 5)
       out += (int64_t)kShortBatch * D;
     }
   };
-  const float2 k2 = unpack(ncs);
-  if (__all_sync(__activemask(), fminf(k2.x, k2.y) >= -0.5f)) run(std::true_type());
+  if (__all_sync(__activemask(), near(unpack(ncs)))) run(std::true_type());
   else run(std::false_type());
   if (h_out != nullptr) *reinterpret_cast<float2 *>(h_out + row * D + d) = unpack(h);
 }

@@ -127,7 +127,7 @@ __device__ __forceinline__ F2 sigmoid2(F2 x) {
   return f2(rcp(q.x), rcp(q.y));
 }
 
-// 2^f - 1 = f P(f) for |f| <= 1/2; P of degree 5, fitted here to 1.1e-8 of its value.
+// 2^f - 1 = f P(f) for |f| <= 1/2; P of degree 5, fitted here to 2.1e-8 of its value.
 __device__ __forceinline__ F2 exp2m1(F2 f) {
   F2 q = fma2(f, f2(1.5403507859446108e-4f), f2(1.3390735257416964e-3f));
   q = fma2(f, q, f2(9.618237614631653e-3f));
@@ -137,8 +137,11 @@ __device__ __forceinline__ F2 exp2m1(F2 f) {
 }
 
 // a = 2^t and less = a - 1 for t <= 0, both to a few half-steps relative to themselves.
-// NEAR: t >= -1/2 for every channel of the warp (its lam's), so that a > 0.7; else
-// t = k + f and a - 1 = 2^k (2^f - 1) + (2^k - 1), which cancels nowhere.
+// NEAR: t > -1/2 for every channel of the warp, so that a > 0.7; else t = k + f and
+// a - 1 = 2^k (2^f - 1) + (2^k - 1), which cancels nowhere.  Where t > -1/2 the second way
+// has k = 0 and rounds as the first does: a channel's numbers do not depend on its warp's
+// others.  (near: of -c softplus(lam) log2(e), which times a gate of one or a step above is t.)
+__device__ __forceinline__ bool near(float2 ncs) { return fminf(ncs.x, ncs.y) >= -0.4999995f; }
 template <bool NEAR> __device__ __forceinline__ void decay2(F2 t, F2 *a, F2 *less) {
   if (NEAR) {
     *less = exp2m1(t);

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, (kCarryResident<T, GATED>))
     constexpr int kChunks = S::kTokens / kGsChunk;  // of a thread
     float4 maps_of[kChunks], map;
     bool resets = false;
-    const bool close = __all_sync(0xffffffffu, fminf(ncs.x, ncs.y) >= -0.5f);
+    const bool close = __all_sync(0xffffffffu, near(ncs));
 #pragma unroll
     for (int c = kChunks - 1; c >= 0; --c) {
       const int at = first + c * kGsChunk;
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kApplyThreads, (kApplyResident<T, GATED>))
     F2 dl = f2(0.0f);
     if (there && first < n) {
       const float2 nn = *reinterpret_cast<const float2 *>(&sm.ncs[s][2 * lane]);
-      bool fast = fminf(nn.x, nn.y) >= -0.5f && n - first >= kGsChunk && d < p.D;
+      bool fast = near(nn) && n - first >= kGsChunk && d < p.D;
       if (PACKED) fast = fast && !(lane < kGsChunk && (sm.marks[s][first + lane % kGsChunk] & 3));
       if (__all_sync(0xffffffffu, fast))
         dl = apply_tokens<T, GATED, PACKED, true>(sm, s, q, row, t0, n, first, lane, d);

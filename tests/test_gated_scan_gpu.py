@@ -733,3 +733,34 @@ def test_gradients_of_saturated_gates(lam):
            "r": (3 + 2 * (1 - la)) * K + K + 2 * np.abs(rd) + 8}
     for k, w in want.items():
         _check(gr[k], w, off[k] * GS.U * np.abs(w) + 1e-37, f"d{k}")
+
+
+def test_equal_short_rows_are_equal_whatever_their_place():
+    """Rows of 36 channel pairs share warps with their neighbours in the kernel of short rows; which
+    arithmetic a decay takes must not depend on who else is in the warp.  Decays whose exponent is
+    within steps of the border of -1/2 (lam a step of fp32 after the other), gates fully open, and
+    eight channels far beyond it."""
+    D, L, n = 72, 16, 64
+    lam = np.full(D, 3.0, np.float32)
+    at = np.float32(0.3)
+    c = np.float32(0.5 / (np.log1p(np.exp(np.float64(at))) * np.log2(np.e)))
+    for i in range(64):
+        lam[i] = at + np.float32(2.0 ** -25 * (i - 32))
+    gen = torch.Generator().manual_seed(73)
+    row = lambda f: f(torch.randn(1, L, D, generator=gen)).expand(n, L, D).contiguous().cuda()  # noqa: E731
+    x, g = row(lambda t: t), row(lambda t: t)
+    r = row(lambda t: 20 + t)
+    h0 = torch.randn(1, D, generator=gen).expand(n, D).contiguous().cuda()
+    dims = m2.make_gated_scan_dims(n, L, D, io_dtype="f32", decay_scale=float(c))
+    lam = torch.from_numpy(lam).cuda()
+    h = h0.clone()
+    y = m2.gated_scan_prefill(dims, lam, x, r, g, h_state=h, states_in=True)
+    assert torch.equal(y, y[:1].expand_as(y))
+    assert torch.equal(h, h[:1].expand_as(h))
+    # and as single tokens
+    s = h0.clone()
+    one = m2.make_gated_scan_dims(n, 1, D, io_dtype="f32", decay_scale=float(c))
+    for t in range(L):
+        yt = m2.gated_scan_step(one, lam, *[v[:, t].contiguous() for v in (x, r, g)], s)
+        assert torch.equal(yt, y[:, t]), t
+    assert torch.equal(s, h)
