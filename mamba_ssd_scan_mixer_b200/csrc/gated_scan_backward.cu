@@ -337,16 +337,17 @@ __global__ void __launch_bounds__(kApplyThreads, (kApplyResident<T, GATED>))
   S &sm = *reinterpret_cast<S *>(raw);
   const Scan &p = q.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (test_stall(&g_gs_stall, &g_gs_errors)) return;
+  const bool stalled = test_stall(&g_gs_stall, &g_gs_errors);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) mbar_init(&sm.full[s], 1);
     sm.dead = 0;
     fence_mbar_init();
   }
   __syncthreads();
+  // (every block waits, so that what waits for this kernel has waited for the one before)
   grid_dependency_wait();
   launch_dependents();
-  if (PACKED && *p.bad) return;
+  if (stalled || (PACKED && *p.bad)) return;
   const int64_t nch = (p.L + kGsChunk - 1) / kGsChunk;
   // one thread: a tile's copies, into stage s
   auto fetch = [&](int s, const Walk &w) {
