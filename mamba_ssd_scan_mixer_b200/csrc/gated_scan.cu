@@ -102,7 +102,8 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
   const int first = seg * S::kTokens;
   for (int it = 0;; ++it) {
     const int s = it % S::kStages, half = it & 1;
-    if (!mbar_wait_parked(&sm.full[s], (it / S::kStages) & 1, &g_gs_errors)) sm.dead = 1;
+    const bool there = mbar_wait_parked(&sm.full[s], (it / S::kStages) & 1, &g_gs_errors);
+    if (!there) sm.dead = 1;  // (the error is raised: what comes of the old contents does not matter)
     const Tile q = sm.tile[s];
     if (q.left <= 0) return;
     const int t0 = q.step * S::kTile, n = (int)min((int64_t)S::kTile, p.L - t0);
@@ -117,7 +118,9 @@ __global__ void __launch_bounds__(kThreads, kResident<GATED>)
     bool whole = true;  // (no sequence begins in either half)
     int owner = 0;      // of the first of the ends
     if (PACKED) {
-      const int mark = lane < min(S::kTokens, n - first) ? marks[lane] : 0, up = threadIdx.x & 16;
+      // (marks that did not come name no sequence)
+      const int mark = there && lane < min(S::kTokens, n - first) ? marks[lane] : 0;
+      const int up = threadIdx.x & 16;
       begins = __ballot_sync(0xffffffffu, mark & kFirst);
       ends = __ballot_sync(0xffffffffu, h_out != nullptr && (mark & kLast));
       whole = begins == 0;

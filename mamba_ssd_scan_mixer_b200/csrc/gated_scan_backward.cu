@@ -100,7 +100,8 @@ __global__ void __launch_bounds__(kThreads, (kCarryResident<T, GATED>))
   const int64_t nch = (p.L + kGsChunk - 1) / kGsChunk;
   for (int it = 0;; ++it) {
     const int s = it % S::kStages, half = it & 1;
-    if (!mbar_wait_parked(&sm.full[s], (it / S::kStages) & 1, &g_gs_errors)) sm.dead = 1;
+    const bool there = mbar_wait_parked(&sm.full[s], (it / S::kStages) & 1, &g_gs_errors);
+    if (!there) sm.dead = 1;  // (the error is raised: what comes of the old contents does not matter)
     const Tile q = sm.tile[s];
     if (q.left <= 0) return;
     const int t0 = (p.steps - 1 - q.step) * S::kTile, n = (int)min((int64_t)S::kTile, p.L - t0);
@@ -118,7 +119,9 @@ __global__ void __launch_bounds__(kThreads, (kCarryResident<T, GATED>))
       const int *marks = sm.marks[s] + at;
       unsigned int lasts = 0;
       if (PACKED)
-        lasts = __ballot_sync(0xffffffffu, lane < min(kGsChunk, n - at) && (marks[lane] & kLast));
+        // (marks that did not come name no sequence)
+        lasts = __ballot_sync(0xffffffffu,
+                              there && lane < min(kGsChunk, n - at) && (marks[lane] & kLast));
       const bool whole = lasts == 0;  // (no sequence ends in either half)
       resets |= !whole;
       lasts = lasts >> (threadIdx.x & 16) & 0xffff;

@@ -34,3 +34,19 @@ def test_the_shared_start_waits_on_every_way():
         text = re.sub(r"//[^\n]*", "", f.read())
     body = text[text.index("bool begin("):]
     assert "return" not in body[:body.index("grid_dependency_wait()")]
+
+
+def test_marks_that_did_not_come_are_not_used():
+    # a mark holds a sequence's number, an index into the states: where the wait for a stage's
+    # copies ran out, the stage may hold anything
+    seen = 0
+    for name, body in _kernels():
+        body = body.split("__global__")[0]
+        if "mbar_wait_parked(&sm.full[s]" not in body:
+            continue
+        assert "const bool there = mbar_wait_parked(&sm.full[s]" in body, name
+        for m in re.finditer(r"[^;{}]*\b(?:sm\.marks\[s\]\[first|marks\[lane\])", body):
+            seen += 1
+            inside = "there &&" in m.group(0) or re.search(r"if \(there && [^\n]*\{\n", body[:m.start()])
+            assert inside, (name, m.group(0))
+    assert seen == 3
