@@ -107,3 +107,35 @@ def backward(lam, x, r, g, dy, z=None, h0=None, dh=None, c=8.0):
     # the terms' errors, and those of summing 128 tokens and then the pieces
     out["lam_off"] = sl * (R * (dla_off + (KAPPA + 128 + L / 128) * U * dM * k_size)).sum(0)
     return out
+
+
+def memory_bounds(lam, x, r, g, h0, dy, dh, c=8.0):
+    """Closer bounds for long memories, where `forward` and `backward` allow KAPPA half-steps of
+    the whole state at every token: of h (each token's), of d_x and of d_h0 in half-steps counted
+    one by one, for |r|, |g| <= 4 and decays near one.
+
+    a = 1 - (1 - a): one rounding of a number in [1/2, 1), half a half-step, and (1 - a) off by
+    KAPPA of itself (R: |r| + 7, c softplus(lam) log2(e): 10, their product 1, the polynomial 9).
+    Between a token and the state that it enters there is one rounding a token, in the fused
+    multiply-add or in the product of a tile's decays: with a's own, 1.5 a token.  Putting
+    segments together adds two for every 8 tokens at most (16 in bf16): 2 a token in all, and 8
+    once for the parts that the last state is put together from.  b is off by KAPPA.  Back,
+    e = a (e + dy) is rounded twice a token: 2.5, and the same for the parts: 3."""
+    R, G, la, a, m = _gates(lam, r, g, c)
+    b = np.abs(m * G * x)
+    M, E = np.abs(h0.astype(np.float64)), np.zeros(len(lam))
+    h_off = np.empty(x.shape)
+    for t in range(len(x)):
+        before = M
+        M = a[t] * M + b[t]
+        E = a[t] * E + U * (2 * M + KAPPA * ((1 - a[t]) * before + b[t]))
+        h_off[t] = E + 8 * U * M
+    dM, dE = np.abs(dh.astype(np.float64)), np.zeros(len(lam))
+    dx_off = np.empty(x.shape)
+    for t in range(len(x) - 1, -1, -1):
+        dM = dM + np.abs(dy[t])
+        dE = dE + U * dM
+        dx_off[t] = m[t] * G[t] * (dE + (KAPPA + 8) * U * dM)
+        dE = a[t] * dE + U * (2 * a[t] + KAPPA * (1 - a[t])) * dM
+        dM = a[t] * dM
+    return {"h_off": h_off, "x_off": dx_off, "h0_off": dE + 8 * U * dM}

@@ -764,3 +764,26 @@ def test_equal_short_rows_are_equal_whatever_their_place():
         yt = m2.gated_scan_step(one, lam, *[v[:, t].contiguous() for v in (x, r, g)], s)
         assert torch.equal(yt, y[:, t]), t
     assert torch.equal(s, h)
+
+
+@pytest.mark.parametrize("batch,L,D", [(1, 6000, 64), (8, 2500, 104)])
+def test_long_memories(batch, L, D):
+    # decays of 0.99 to 0.9995 and inputs of one sign, against bounds counted rounding by rounding
+    gen = torch.Generator().manual_seed(74)
+    pos = lambda *s: torch.randn(*s, generator=gen).abs().cuda()  # noqa: E731
+    gate = lambda: (1 + 0.5 * torch.randn(batch, L, D, generator=gen)).clamp(-4, 4).cuda()  # noqa: E731
+    v = {"x": pos(batch, L, D), "r": gate(), "g": gate(), "z": None, "dy": pos(batch, L, D)}
+    u = torch.linspace(0.99, 0.9995, D, dtype=torch.float64)
+    v["lam"] = torch.log(torch.expm1(-torch.log(u) / C)).float().cuda()
+    h0, dh = pos(batch, D), pos(batch, D)
+    y, h, gr = _run(v, [L] * batch, D, "f32", False, h0, dh)
+    lam = _np(v["lam"])
+    for i in range(batch):
+        x, r, g, dy = (_np(v[k][i]) for k in ("x", "r", "g", "dy"))
+        off = GS.memory_bounds(lam, x, r, g, _np(h0[i]), dy, _np(dh[i]), C)
+        f = GS.forward(lam, x, r, g, None, _np(h0[i]), C)
+        b = GS.backward(lam, x, r, g, dy, None, _np(h0[i]), _np(dh[i]), C)
+        _check(y[i], f["h"], off["h_off"], f"y of row {i}")
+        _check(h[i], f["h_end"], off["h_off"][-1], f"final state {i}")
+        _check(gr["x"][i], b["x"], off["x_off"], f"dx of row {i}")
+        _check(gr["h_state"][i], b["h0"], off["h0_off"], f"dh0 of row {i}")

@@ -64,3 +64,31 @@ def test_bounds_are_small_beside_the_results():
     v = _inputs(300, 5, 3)
     f = GS.forward(v["lam"], v["x"], v["r"], v["g"], v["z"], v["h0"])
     assert np.max(f["y_off"]) < 1e-3 * np.max(np.abs(f["y"]))
+
+
+def _long(L=3000, D=8, seed=9):
+    """Decays from 0.99 to 0.9995 and inputs of one sign: nothing cancels, and every error stays."""
+    g = np.random.default_rng(seed)
+    v = {k: np.abs(g.standard_normal((L, D))) for k in ("x", "dy")}
+    v["r"], v["g"] = (np.clip(1 + 0.5 * g.standard_normal((L, D)), -4, 4) for _ in range(2))
+    v["lam"] = np.log(np.expm1(-np.log(np.linspace(0.99, 0.9995, D)) / 8.0))
+    v["h0"], v["dh"] = np.abs(g.standard_normal(D)), np.abs(g.standard_normal(D))
+    return {k: t.astype(np.float32).astype(np.float64) for k, t in v.items()}
+
+
+def test_closer_bounds_hold_for_fp32_and_see_three_lost_digits():
+    v = _long()
+    near = GS.memory_bounds(**v)
+    f = GS.forward(v["lam"], v["x"], v["r"], v["g"], None, v["h0"])
+    # token by token in fp32, from coefficients rounded to it
+    _, G, _, a, m = GS._gates(v["lam"], v["r"], v["g"], 8.0)
+    a32, b32 = a.astype(np.float32), (m * G * v["x"]).astype(np.float32)
+    h, worst = v["h0"].astype(np.float32), 0.0
+    for t in range(len(a32)):
+        h = (a32[t] * h + b32[t]).astype(np.float32)
+        worst = max(worst, np.max(np.abs(h - f["h"][t]) / near["h_off"][t]))
+    assert worst < 1
+    # a state that has lost three of its digits halfway: the wide bounds let it pass
+    lost = f["h"] * (1 + 2.0 ** -12)
+    assert np.all(np.abs(lost - f["h"])[-1, -1] <= f["h_off"][-1, -1])
+    assert np.all(np.abs(lost - f["h"]) > near["h_off"])
