@@ -366,8 +366,10 @@ MAMBA2_API int mamba2_conv_ssd_prefill_backward(
  *     a_t = exp(-c s R_t)
  *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) G_t x_t
  *     y_t = h_t, or h_t silu(z_t) where a gate z is given.
- * x, r, g and z are the layer's projections, biases included.  The state is
- * fp32 and owned by the caller, as the SSM state is. */
+ * x, r, g and z are the layer's projections, biases included.  A sequence's first
+ * token is scaled by sqrt(1 - a_t^2) like every other (there is no form with a
+ * factor of one there).  The state is fp32 and owned by the caller, as the SSM
+ * state is. */
 
 /* Tokens of a checkpoint (see mamba2_gated_scan_prefill). */
 #define MAMBA2_GATED_SCAN_CHUNK 16
@@ -405,7 +407,8 @@ MAMBA2_API size_t mamba2_gated_scan_checkpoint_count(const mamba2_gated_scan_dim
  *          cu_seqlens[s] .. cu_seqlens[s + 1] - 1: 0, then the running counts,
  *          last = L; empty sequences are allowed.  Offsets that break this are
  *          found on the device: the call then writes nothing and
- *          mamba2_device_errors reports bit 2.
+ *          mamba2_device_errors reports bit 2.  (With L = 0 every sequence is
+ *          empty, and they are not read.)
  *  y       [b, L, D] io_dtype, contiguous, 16-byte aligned.  Output.
  *  h_state [b, D] fp32, contiguous, 16-byte aligned, or NULL: when states_in != 0
  *          the state entering the first token (else it is zero); on return the
@@ -421,7 +424,9 @@ MAMBA2_API size_t mamba2_gated_scan_checkpoint_count(const mamba2_gated_scan_dim
  * 64 tokens may be summed in another order in a large batch than in a small one.)
  * Range: a gate sigmoid below 2^-62 counts as 2^-62, and where 1 - a^2 is below
  * 2^-56 nothing is added: r = -infinity keeps a state as it is (for c softplus(lam)
- * < 32).  NaN and infinities stay within their sequence and channel. */
+ * < 32).  NaN and infinities stay within their sequence and channel; from an
+ * infinite state on, y and the state are infinite or NaN (a stretch of decays may
+ * multiply to zero, and zero times infinity is NaN). */
 MAMBA2_API int mamba2_gated_scan_prefill(
     const mamba2_gated_scan_dims *dims, const float *lam, const void *x, int64_t x_row_stride,
     const void *r, int64_t r_row_stride, const void *g, int64_t g_row_stride, const void *z,

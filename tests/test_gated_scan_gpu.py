@@ -787,3 +787,30 @@ def test_long_memories(batch, L, D):
         _check(h[i], f["h_end"], off["h_off"][-1], f"final state {i}")
         _check(gr["x"][i], b["x"], off["x_off"], f"dx of row {i}")
         _check(gr["h_state"][i], b["h0"], off["h0_off"], f"dh0 of row {i}")
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_infinite_states_stay_in_their_channel(packed):
+    # (a tile's decays multiply to zero, and zero times infinity is NaN: not finite is all that
+    # holds for the channel itself)
+    D, lens = 40, [500, 3, 397]
+    lam = torch.linspace(-3, 6, D)
+    v = _inputs(None, sum(lens), D, 75, "f32", False, lam=lam)
+    if not packed:
+        v = {k: (t if t is None or k == "lam" else t[None]) for k, t in v.items()}
+        lens = [900]
+    h0, dh = _states(len(lens), D, 76)
+    y, h, gr = _run(v, lens, D, "f32", packed, h0, dh)
+    bad = h0.clone()
+    bad[0, ::4] = float("inf")
+    y2, h2, gr2 = _run(v, lens, D, "f32", packed, bad, dh)
+    own = torch.zeros(D, dtype=torch.bool, device="cuda")
+    own[::4] = True
+    one, two = (t.reshape(-1, D) for t in (y, y2))
+    n = lens[0]
+    assert not torch.isfinite(two[:n, own]).any() and not torch.isfinite(h2[0, own]).any()
+    assert torch.equal(one[:n, ~own], two[:n, ~own]) and torch.equal(one[n:], two[n:])
+    assert torch.equal(h[0, ~own], h2[0, ~own]) and torch.equal(h[1:], h2[1:])
+    for k in ("x", "g", "r"):
+        assert torch.equal(gr[k].reshape(-1, D)[:, ~own], gr2[k].reshape(-1, D)[:, ~own]), k
+        assert torch.equal(gr[k].reshape(-1, D)[n:], gr2[k].reshape(-1, D)[n:]), k
