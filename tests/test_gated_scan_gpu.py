@@ -814,3 +814,49 @@ def test_infinite_states_stay_in_their_channel(packed):
     for k in ("x", "g", "r"):
         assert torch.equal(gr[k].reshape(-1, D)[:, ~own], gr2[k].reshape(-1, D)[:, ~own]), k
         assert torch.equal(gr[k].reshape(-1, D)[n:], gr2[k].reshape(-1, D)[n:]), k
+
+
+def test_a_captured_fork_and_join():
+    # two prompts on two streams of one capture, copies before them and a cache and a step behind
+    # the join; replayed on other inputs, against the same calls made one by one
+    D, L = 136, 900
+    dims = m2.make_gated_scan_dims(1, L, D)
+    one = m2.make_gated_scan_dims(2, 1, D)
+    sets = [[_inputs(1, L, D, 80 + 2 * i + k, "bf16", False) for k in range(2)] for i in range(2)]
+    slots = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+
+    def run(ins, fork):
+        main = torch.cuda.current_stream()
+        other = side if fork else main
+        h, back = torch.zeros(2, D, device="cuda"), torch.zeros(2, D, device="cuda")
+        codes, scales = m2.state_cache(2, D)
+        other.wait_stream(main)
+        ys = []
+        for k, s in ((0, main), (1, other)):
+            with torch.cuda.stream(s):
+                v = {n: t.clone() for n, t in ins[k].items() if n in ("lam", "x", "r", "g")}
+                ys.append(m2.gated_scan_prefill(dims, v["lam"], v["x"], v["r"], v["g"],
+                                                h_state=h[k:k + 1]))
+        main.wait_stream(other)
+        m2.state_cache_store(h, slots, codes, scales)
+        m2.state_cache_load(codes, scales, slots, back)
+        last = [torch.cat([ins[k][n][:, -1] for k in range(2)]) for n in ("x", "r", "g")]
+        ys.append(m2.gated_scan_step(one, ins[0]["lam"], *last, back))
+        return [*ys, h, back]
+
+    want = [run(s, False) for s in sets]
+    torch.cuda.synchronize()
+    live = [{n: (None if t is None else t.clone()) for n, t in v.items()} for v in sets[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(live, True)
+    for i in (1, 0, 1):
+        for a, b in zip(live, sets[i]):
+            for n, t in a.items():
+                if t is not None:
+                    t.copy_(b[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want[i], out)), i
+    assert m2.device_errors() == 0
