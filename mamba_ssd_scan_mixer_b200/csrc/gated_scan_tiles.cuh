@@ -122,11 +122,27 @@ __global__ void gs_prep_kernel(const float *lam, float c, int D, float *ncs, uin
     }
     marks[t] = (int)(lo << 2) | (cu[lo] == t ? kFirst : 0) | (cu[lo + 1] - 1 == t ? kLast : 0);
   }
-  if (empty_out != nullptr)
-    for (int64_t s = at / 32; s < batch; s += all / 32)  // a warp for a sequence
-      if (cu[s + 1] == cu[s])
-        for (int d = threadIdx.x % 32; d < D; d += 32)
-          empty_out[s * D + d] = empty_in != nullptr ? empty_in[s * D + d] : 0.0f;
+  if (empty_out == nullptr) return;
+  // a warp for 1024 channels of a sequence, all read before any is written: one warp for a whole
+  // row, 32 channels after the other, took 54 us for one empty sequence of 4096 channels
+  constexpr int kQuads = 8;
+  const int pieces = (D + 128 * kQuads - 1) / (128 * kQuads);
+  const int64_t warp = at / 32, together = all / 32 / pieces;  // sequences looked at at once
+  const int d0 = (int)(warp % pieces) * (128 * kQuads) + 4 * (threadIdx.x % 32);
+  if (warp >= together * pieces) return;
+  for (int64_t s = warp / pieces; s < batch; s += together) {
+    if (cu[s + 1] != cu[s]) continue;
+    float4 v[kQuads];
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) {
+      v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (empty_in != nullptr && d0 + 128 * k < D)
+        v[k] = *reinterpret_cast<const float4 *>(empty_in + s * D + d0 + 128 * k);
+    }
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k)
+      if (d0 + 128 * k < D) *reinterpret_cast<float4 *>(empty_out + s * D + d0 + 128 * k) = v[k];
+  }
 }
 
 // The block's named barriers.  All wait in hardware: warps that ask an mbarrier again and

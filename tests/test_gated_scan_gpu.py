@@ -860,3 +860,46 @@ def test_a_captured_fork_and_join():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want[i], out)), i
     assert m2.device_errors() == 0
+
+
+@pytest.mark.parametrize("D", [8, 1000, 1024, 1032, 5120])
+def test_empty_sequences_hand_their_states_on(D):
+    # a copy of d_h_state_out in pieces of a row; with states_in false the state is zero
+    lens = [0, 5, 0, 0, 70, 0]
+    v = _inputs(None, sum(lens), D, 90, "f32", False)
+    h0, dh = _states(len(lens), D, 91)
+    y, h, gr = _run(v, lens, D, "f32", True, h0, dh)
+    zero = _run(v, lens, D, "f32", True, None, None)[1]
+    for i, n in enumerate(lens):
+        if n == 0:
+            assert torch.equal(h[i], h0[i]) and torch.equal(gr["h_state"][i], dh[i]), i
+            assert torch.count_nonzero(zero[i]) == 0, i
+
+
+def test_an_empty_sequence_costs_next_to_nothing():
+    # (one warp that copied a row's state 32 channels after the other took 0.33 ms here)
+    D, L = 65536, 64
+    v = _inputs(None, L, D, 92, "bf16", False)
+    dims = m2.make_gated_scan_dims(2, L, D)
+    h0, dh = _states(2, D, 93)
+    ck = m2.gated_scan_checkpoints(dims, True)
+
+    def took(cu):
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        best = float("inf")
+        for _ in range(10):
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            e[0].record()
+            for _ in range(5):
+                m2.gated_scan_backward(dims, v["lam"], v["x"], v["r"], v["g"], v["dy"], h_state_in=h0,
+                                       d_h_state_out=dh, cu_seqlens=c, checkpoints=ck)
+            e[1].record()
+            torch.cuda.synchronize()
+            best = min(best, e[0].elapsed_time(e[1]) / 5 * 1000)
+        return best
+
+    m2.gated_scan_prefill(dims, v["lam"], v["x"], v["r"], v["g"], h_state=h0.clone(), states_in=True,
+                          cu_seqlens=torch.tensor([0, 30, L], dtype=torch.int32, device="cuda"),
+                          checkpoints=ck)
+    full, empty = took([0, 30, L]), took([0, 0, L])
+    assert empty < full + 200, (empty, full)
