@@ -5,8 +5,8 @@
 The library is plain CUDA C++ with a C ABI (include/mamba2ssd.h); it links
 the CUDA runtime statically and needs no PyTorch at build time.  --checked
 also builds libmamba2ssd_checked.so, the same library compiled with
--DMAMBA2_BOUNDS_CHECK: every plain global access of the tensor-core prefill and
-decode kernels is checked against its buffer's extent and alignment, skipped if
+-DMAMBA2_BOUNDS_CHECK: every plain global access of the mixer's tensor-core
+prefill and decode kernels is checked against its buffer's extent and alignment, skipped if
 it fails, and reported by mamba2_device_errors (bit 1).  Load it by setting
 MAMBA2SSD_LIBRARY to its path before importing the binding.
 """

@@ -21,7 +21,8 @@
 // channels, bf16: 240 us, 85% of the copy rate; one row in fp32: 57 us, 89%).  In one bf16
 // row the tiles under way reach over four steps of the row, and each waits about a
 // microsecond a round for the map of the one before (43 us, 60%).  Next to that come the
-// instructions: 47 a pair of channels and token, eight of them ex2, rcp or sqrt.
+// instructions: 71 a pair of channels and token with those of the waits, eight of them ex2,
+// rcp or sqrt.
 #include "gated_scan_tiles.cuh"
 
 namespace m2 {

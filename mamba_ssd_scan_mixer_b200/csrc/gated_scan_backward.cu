@@ -17,13 +17,15 @@
 //      its 16 tokens forwards, keeping h, e^-r and e^-g, and backwards.
 // The first pass costs 4 bytes an element beside the second's 14 (bf16).  (The second
 // begins where the first ended, and finds 29 of 84 MB of r and dy in L2 at 4096 tokens of
-// 5120 channels.)  One pass over everything would have to keep a tile's coefficients while
-// the E entering it is looked up, which halves the tiles under way.
+// 5120 channels.)  Two passes, since the second then waits for nothing and the first, which
+// waits, holds little.  (One pass whose sweep forwards runs while E is on its way would read
+// r and dy once; it has not been built.)
 //
 // 4096 tokens of 5120 channels, bf16: the first 27 us (13 at the copy rate), the second
-// 65 us (46).  The first waits for the maps of the tiles before, as the prefill does.  The
-// second issues 114 instructions a pair of channels and token, 12 of them ex2, rcp or sqrt,
-// at 55% of the issue rate with the 12 warps that its registers leave.
+// 67 us (46).  The first waits for the maps of the tiles before, as the prefill does.  The
+// second issues 119 instructions a pair of channels and token, 14 of them ex2, rcp or sqrt,
+// at half of the issue rate with the 12 warps that its registers leave.  (With z, 8 warps: two
+// stages leave room for two blocks.)
 #include "gated_scan_tiles.cuh"
 
 namespace m2 {

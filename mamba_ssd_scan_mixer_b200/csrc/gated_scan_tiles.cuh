@@ -16,7 +16,7 @@ namespace {
 
 // Channels of a tile: half a warp takes two each.  (Wider tiles would be shorter: more of
 // a row's tiles, each waiting for the one before, would be under way at once.  64 channels
-// by 64 tokens: 475 against 447 us at 32768 tokens of 7168 channels with z.)
+// by 64 tokens: 475 against 447 us at 32768 tokens of 7168 channels with z, before the power cap.)
 constexpr int kWidth = 32;
 constexpr int kLanes = kWidth / 2;
 constexpr int kWarps = 4;           // that compute

@@ -94,7 +94,8 @@ __device__ __forceinline__ int64_t slot_of(const int32_t *slots, int64_t b, int6
 }
 // Whether a later row names slot s too (then this row is not written).  Each block
 // reads the rest of the slots: 4 bytes a row, small beside a state of thousands of
-// values for batches of the usual size.
+// values for batches of hundreds (4096 rows of 8192 values: 39 us, 26 at the copy rate; 65535
+// rows of 512: 840 us, 26).
 __device__ __forceinline__ bool named_later(const int32_t *slots, int64_t b, int64_t batch,
                                             int64_t s) {
   int later = 0;
